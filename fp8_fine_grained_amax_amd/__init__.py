@@ -61,6 +61,7 @@ def lib():
         L.fg_status_string.restype = ctypes.c_char_p
         L.fg_last_hip_error.argtypes = []
         L.fg_last_hip_error.restype = I
+        ffn.declare(L)
         _lib = L
     return _lib
 
@@ -385,3 +386,8 @@ def fg_fp8_grouped_gemm_wgrad(dytq, sdyt, xtq, sxt, offsets, dw=None, accumulate
                                            _ptr(dw), int(bool(accumulate)), _mode(pow2), _stream(dytq.device)),
            "fg_fp8_grouped_gemm_wgrad")
     return dw
+
+
+from . import ffn  # noqa: E402  (it uses this module's helpers)
+from .ffn import (FG_ACT_GELU_TANH, FG_ACT_NONE, FG_ACT_RELU, FG_ACT_SILU, ActGrad,  # noqa: E402,F401
+                  fg_act_checkpoint_bwd, fg_act_checkpoint_fwd, fg_fp8_gemm_fprop_epilogue, fg_moe_few_tokens)

@@ -11,7 +11,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8fg.so")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip", "per_tensor.hip", "e5m6.hip", "limited_accum.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "per_tensor.hip", "e5m6.hip", "limited_accum.hip", "act_checkpoint.hip",
+           "few_tokens.hip"]
+HOST_SOURCES = ["ffn_api.cpp"]          # argument checks only: no device code
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -21,11 +23,16 @@ def flags():
             "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
+def host_flags():
+    return ["-O2", "-std=c++17", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
+
+
 def build(verbose: bool = False, extra=()) -> str:
     objs = []
-    for src in SOURCES:
-        obj = os.path.join(CSRC, src.replace(".hip", ".o"))
-        cmd = [HIPCC, *flags(), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    for src in SOURCES + HOST_SOURCES:
+        obj = os.path.join(CSRC, os.path.splitext(src)[0] + ".o")
+        dev = [*flags(), *extra] if src in SOURCES else host_flags()
+        cmd = [HIPCC, *dev, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)

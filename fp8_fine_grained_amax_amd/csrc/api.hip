@@ -87,6 +87,9 @@ bool too_many_tiles(int64_t a, int64_t b) { return prod_over(cdiv(a, 256), cdiv(
 
 }  // namespace
 
+// The same for the entry points of ffn_api.cpp: one record per thread for the whole library.
+fg_status fg_status_from_hip(hipError_t e) { return from_hip(e); }
+
 extern "C" {
 
 fg_status fg_quantize_e5m6_1x128(const void* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* packed,

@@ -42,6 +42,8 @@
 #include <string.h>
 
 #include "common.h"
+#include "ffn_launch.h"
+#include "ffn_math.h"
 #include "host_util.h"
 
 namespace {
@@ -75,7 +77,7 @@ using Cfg8 = TileCfg<2, 4, 128, 64>;   // 256 x 256
 
 enum { SB_BLOCK = 0, SB_BLOCK_T = 1, SB_ROW = 2 };
 enum { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
-enum { EPI_STORE = 0, EPI_QUANT = 1 };
+enum { EPI_STORE = 0, EPI_QUANT = 1, EPI_ACT = 2 };
 
 struct GemmParams {
     const uint8_t* a;       // A-role codes [rows][K], row stride K
@@ -95,6 +97,7 @@ struct GemmParams {
     uint8_t* q_out;           // EPI_QUANT: E4M3 codes of the BF16 output [M][N]
     float* s_out;             // EPI_QUANT: their 1x128 scales [N/128][M]
     int q_pow2;               // EPI_QUANT: power-of-2 output scales
+    FgEpilogue ep;            // EPI_ACT: bias, activation, residual
 };
 
 // LDS swizzles. gfx950 serves a ds_read_b128 16 lanes (256 B, all 64 banks) at a time, and the 8 rows
@@ -787,6 +790,27 @@ __global__ __launch_bounds__(C::NTHREADS, 1) void fg_gemm_kernel(GemmParams p) {
         }
         return;
     }
+    if constexpr (EPI == EPI_ACT) {
+        // act(acc + bias) + residual in the MFMA layout, on the fp32 sums; the store below rounds once.
+#pragma unroll
+        for (int j = 0; j < NSUB; j++) {
+            const int64_t n = wave_n0 + j * 16 + lcol4;
+            float b[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) b[r] = p.ep.bias && n + r < N ? fg_load_elem(p.ep.bias, n + r, p.ep.bias_bf16) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < MSUB; i++) {
+                const int64_t m = m0 + wm * WAVE_M + i * 16 + lrow;
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    float v = fg_act_any(p.ep.act, acc[i][j][r] + b[r]);
+                    if (p.ep.residual && m < m_end && n + r < N)
+                        v += fg_load_elem(p.ep.residual, m * p.ep.ld_res + n + r, p.ep.residual_bf16);
+                    acc[i][j][r] = v;
+                }
+            }
+        }
+    }
     if constexpr (NW == 8 && WAVE_M == 128 && WAVE_N == 64 && C::LDS_BYTES >= NW * 64 * 256) {
         // FP32 output through LDS. In the MFMA layout one 16-byte store per lane writes 16 rows x 64 B, and
         // a compute unit streams such stores at about a third of the rate of stores that write 4 rows x
@@ -1376,6 +1400,22 @@ hipError_t fg_launch_gemm_fprop(const uint8_t* xq, const float* sx, const uint8_
         return pow2 ? launch_wide<true, false>(p, grid, stream) : launch_wide<false, false>(p, grid, stream);
     }
     return launch<false, SB_BLOCK, GRP_NONE>(p, pow2, stream);
+}
+
+hipError_t fg_launch_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
+                                         int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, int pow2,
+                                         hipStream_t stream) {
+    GemmParams p{};
+    p.a = xq; p.sa = sx; p.sa_ld = M; p.b = wq; p.sb = sw;
+    p.M = M; p.N = N; p.K = K; p.out = y; p.out_bf16 = out_bf16; p.ep = e;
+    if (use_cfg8(p, GRP_NONE)) {
+        const unsigned grid = grid_for<Cfg8>(p, GRP_NONE);
+        return pow2 ? launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, true, EPI_ACT>(p, grid, stream)
+                    : launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, false, EPI_ACT>(p, grid, stream);
+    }
+    const unsigned grid = grid_for<Cfg12>(p, GRP_NONE);
+    return pow2 ? launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, true, EPI_ACT>(p, grid, stream)
+                : launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, false, EPI_ACT>(p, grid, stream);
 }
 
 hipError_t fg_launch_gemm_dgrad(const uint8_t* dyq, const float* sdy, const uint8_t* wq, const float* sw, int64_t M,
