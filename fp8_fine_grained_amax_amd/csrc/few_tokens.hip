@@ -8,9 +8,12 @@
 // rows as its first operand and tokens as its second, so lane l ends with token l % 16 and four consecutive
 // weight rows.
 //
-// K order inside a block: lane l of group g = l / 16 holds the bytes [16 g, 16 g + 16) and [64 + 16 g, + 16) of its
-// row's 128, for weights and activations alike, so each load instruction reads 64 contiguous bytes of a row. The
-// block's products are the same ones in another order.
+// Loads and operands: an MFMA operand has row l % 16 and the bytes [16 g, 16 g + 16) and [64 + 16 g, + 16) of its 128,
+// g = l / 16, in lane l. Loaded like that, every lane of a quad reads another row, which a compute unit serves at a
+// third of its rate (L2-resident rows: 9.4 TB/s over the card, against 29 with quads that read 64 contiguous
+// bytes; from HBM 3.9 to 5.2 against 5.1 to 5.8). So lane l loads row l / 4 and the bytes of g = l % 4, and the
+// registers are turned to operands by an exchange over the LDS crossbar (ds_bpermute, eight an operand).
+#include "ffn_epilogue.h"
 #include "ffn_launch.h"
 #include "ffn_math.h"
 #include "host_util.h"
@@ -23,18 +26,36 @@ namespace {
 enum { SRC_BF16 = 0, SRC_F32 = 1, SRC_CODES = 2 };
 constexpr int BK = FG_GROUP;
 
-// One token tile's operand of one K block as it is loaded: this lane's 32 values of its token's 128.
+// A lane's place in a load of a 16-row tile, and the byte address (4 x lane) that an operand lane takes its bytes from.
+__device__ __forceinline__ int load_row(int lane) { return lane >> 2; }
+__device__ __forceinline__ int load_group(int lane) { return lane & 3; }
+__device__ __forceinline__ int operand_source(int lane) { return 4 * (4 * (lane & 15) + (lane >> 4)); }
+
+__device__ __forceinline__ v8i to_operand(const v4i& lo, const v4i& hi, int source) {
+    v8i r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        r[i] = __builtin_amdgcn_ds_bpermute(source, lo[i]);
+        r[4 + i] = __builtin_amdgcn_ds_bpermute(source, hi[i]);
+    }
+    return r;
+}
+
+// Hidden values in the workspace: the 32 values of each lane group g of a row's 128 are eight fours, and four j of
+// all groups lie next to each other, so that the loads of a quad are contiguous there too. Position of the four
+// that begins at k (a multiple of 4).
+__device__ __forceinline__ int hidden_at(int k) { return ((k >> 6) * 4 + ((k >> 2) & 3)) * 16 + ((k >> 4) & 3) * 4; }
+
+// One token tile of one K block as it is loaded: this lane's 32 values of its row's 128. `row` is the load row's.
 template <int SRC>
 struct ActRegs;
 template <>
 struct ActRegs<SRC_BF16> {
     uint4 v[4];
-    __device__ __forceinline__ void load(const uint16_t* row, int64_t k, int g) {
-        const uint16_t* p = row + k + 16 * g;
-        v[0] = *reinterpret_cast<const uint4*>(p);
-        v[1] = *reinterpret_cast<const uint4*>(p + 8);
-        v[2] = *reinterpret_cast<const uint4*>(p + 64);
-        v[3] = *reinterpret_cast<const uint4*>(p + 72);
+    __device__ __forceinline__ void load(const uint16_t* row, int64_t k, int lane) {
+        const uint16_t* p = row + k + 16 * load_group(lane);
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = *reinterpret_cast<const uint4*>(p + (i >> 1) * 64 + (i & 1) * 8);
     }
     __device__ __forceinline__ void get(float (&f)[32]) const {
 #pragma unroll
@@ -51,10 +72,10 @@ struct ActRegs<SRC_BF16> {
 template <>
 struct ActRegs<SRC_F32> {
     v4f v[8];
-    __device__ __forceinline__ void load(const float* row, int64_t k, int g) {
-        const float* p = row + k + 16 * g;
+    __device__ __forceinline__ void load(const float* row, int64_t k, int lane) {
+        const float* p = row + k + 4 * load_group(lane);
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = *reinterpret_cast<const v4f*>(p + (i >> 2) * 64 + (i & 3) * 4);
+        for (int i = 0; i < 8; i++) v[i] = *reinterpret_cast<const v4f*>(p + 16 * i);
     }
     __device__ __forceinline__ void get(float (&f)[32]) const {
 #pragma unroll
@@ -64,43 +85,50 @@ struct ActRegs<SRC_F32> {
 template <>
 struct ActRegs<SRC_CODES> {
     v4i lo, hi;
-    float s;
-    __device__ __forceinline__ void load(const uint8_t* row, const float* scale, int64_t k, int g) {
-        lo = *reinterpret_cast<const v4i*>(row + k + 16 * g);
-        hi = *reinterpret_cast<const v4i*>(row + k + 64 + 16 * g);
+    float s;          // of the operand's row
+    __device__ __forceinline__ void load(const uint8_t* row, const float* scale, int64_t k, int lane) {
+        const uint8_t* p = row + k + 16 * load_group(lane);
+        lo = *reinterpret_cast<const v4i*>(p);
+        hi = *reinterpret_cast<const v4i*>(p + 64);
         s = *scale;
     }
 };
 
-// Max over the four lanes l % 16 + 16 i that hold one token: the two row swaps leave each lane's partner value
-// in one of their two results.
-__device__ __forceinline__ float token_max(float v) {
-    const uint32_t u = __float_as_uint(v);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const float m = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-    return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+// Max over the quad that holds one row (quad_perm [1,0,3,2], [2,3,0,1]).
+__device__ __forceinline__ float quad_max(float v) {
+    v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
+    return __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false)));
 }
 
-// The MFMA operand of a token tile and the lane's token's scale; fp32 and bf16 values are quantized 1x128 here.
+// The MFMA operand of a token tile and the scale of the lane's operand row; fp32 and bf16 values are quantized
+// 1x128 here, as loaded.
 template <int SRC>
-__device__ __forceinline__ v8i act_operand(const ActRegs<SRC>& r, int pow2, float& s) {
+__device__ __forceinline__ v8i act_operand(const ActRegs<SRC>& r, int pow2, int source, float& s) {
     if constexpr (SRC == SRC_CODES) {
         s = r.s;
-        return v8i{r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+        return to_operand(r.lo, r.hi, source);
     } else {
         float f[32];
         r.get(f);
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; i++) m = __builtin_fmaxf(m, __builtin_fabsf(f[i]));
-        s = fg_scale_from_amax(token_max(m), pow2);
-        const fg_divisor d = fg_make_divisor(s, pow2);
-        const int form = fg_quot_form(s, pow2);
-        v8i q;
+        const float own = fg_scale_from_amax(quad_max(m), pow2);
+        // one form for both scale modes: a power-of-2 scale's first quotient is exact and its correction 0
+        fg_divisor d = fg_make_divisor(own, pow2);
+        if (__builtin_amdgcn_ballot_w64(fg_small_scale(own)) != 0 && fg_small_scale(own)) {
+            d = fg_divisor_shifted(d);
 #pragma unroll
-        for (int i = 0; i < 8; i++) q[i] = (int)fg_quant4_any(form, f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], d);
-        return q;
+            for (int i = 0; i < 32; i++) f[i] *= 0x1p64f;
+        }
+        v4i lo, hi;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            lo[i] = (int)fg_quant4<FG_Q_FAST>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], d);
+            hi[i] = (int)fg_quant4<FG_Q_FAST>(f[16 + 4 * i], f[17 + 4 * i], f[18 + 4 * i], f[19 + 4 * i], d);
+        }
+        s = __int_as_float(__builtin_amdgcn_ds_bpermute(source, __float_as_int(own)));
+        return to_operand(lo, hi, source);
     }
 }
 
@@ -113,22 +141,24 @@ struct StepRegs {
     ActRegs<SRC> x[NT];
 };
 
-__device__ __forceinline__ v4i load_weight(const uint8_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const v4i*>(p));   // read once: not worth a place in the caches
-}
+// Not a non-temporal load: the two halves of a line come from two instructions, and only a cached line is fetched once.
+__device__ __forceinline__ v4i load_weight(const uint8_t* p) { return *reinterpret_cast<const v4i*>(p); }
 
 // acc += sW sX P_b for every tile of a step; `tiles` has a bit for each token tile that holds a token in use.
 template <int RT, int SG, int NT, int SRC>
-__device__ __forceinline__ void consume(const StepRegs<RT, SG, NT, SRC>& b, int pow2, int tiles, v4f (&acc)[RT][NT]) {
+__device__ __forceinline__ void consume(const StepRegs<RT, SG, NT, SRC>& b, int pow2, int tiles, int source,
+                                        v4f (&acc)[RT][NT]) {
+    v8i w[RT];
+#pragma unroll
+    for (int r = 0; r < RT; r++) w[r] = to_operand(b.w[r][0], b.w[r][1], source);
 #pragma unroll
     for (int t = 0; t < NT; t++) {
         if (NT > 1 && !((tiles >> t) & 1)) continue;
         float s;
-        const v8i x = act_operand<SRC>(b.x[t], pow2, s);
+        const v8i x = act_operand<SRC>(b.x[t], pow2, source, s);
 #pragma unroll
         for (int r = 0; r < RT; r++) {
-            const v8i w = v8i{b.w[r][0].x, b.w[r][0].y, b.w[r][0].z, b.w[r][0].w, b.w[r][1].x, b.w[r][1].y, b.w[r][1].z, b.w[r][1].w};
-            const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+            const v4f part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[r], x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
             const float f = s * b.ws[r * SG / RT];
 #pragma unroll
             for (int q = 0; q < 4; q++) acc[r][t][q] = __builtin_fmaf(part[q], f, acc[r][t][q]);
@@ -152,8 +182,12 @@ template <int DEPTH, class Regs, class Load, class Use>
 __device__ __forceinline__ void stream_steps(int k0, int k1, Load&& load, Use&& use) {
     Regs buf[DEPTH];
     if (k0 >= k1) return;
+    // The order of the loads is kept by scheduling fences: a wait for one counts the ones behind it.
 #pragma unroll
-    for (int i = 0; i < DEPTH; i++) load(buf[i]);
+    for (int i = 0; i < DEPTH; i++) {
+        load(buf[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     for (int k = k0; k < k1; k += DEPTH) {
 #pragma unroll
         for (int i = 0; i < DEPTH; i++) {
@@ -176,7 +210,7 @@ __global__ __launch_bounds__(NW * 64) void fg_stream_linear_kernel(const uint8_t
                                                                    int out_bf16) {
     __shared__ float red[NW][RT * NT * 4][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4, z = lane_zero();
+    const int l16 = lane & 15, g = lane >> 4, z = lane_zero(), source = operand_source(lane);
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), m0 = (int64_t)blockIdx.y * (16 * NT);
     const int nkb = (int)(K / BK);
     const int k0 = (int)((int64_t)nkb * wave / NW), k1 = (int)((int64_t)nkb * (wave + 1) / NW);
@@ -186,14 +220,14 @@ __global__ __launch_bounds__(NW * 64) void fg_stream_linear_kernel(const uint8_t
     int64_t xm[NT];
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-        const int64_t n = n0 + 16 * r + l16;          // columns past N read the last one again
-        wp[r] = wq + (n < N ? n : N - 1) * K + 16 * g;
+        const int64_t n = n0 + 16 * r + load_row(lane);         // columns past N read the last one again
+        wp[r] = wq + (n < N ? n : N - 1) * K + 16 * load_group(lane);
     }
 #pragma unroll
     for (int t = 0; t < NT; t++) {
-        const int64_t m = m0 + 16 * t + l16;
+        const int64_t m = m0 + 16 * t + l16, r = m0 + 16 * t + load_row(lane);     // and rows past M
         xm[t] = m < M ? m : M - 1;
-        xp[t] = xq + xm[t] * K;
+        xp[t] = xq + (r < M ? r : M - 1) * K;
     }
     const float* sp = sw + (n0 / 128) * nkb + z;
     const int left = (int)((M - m0 + 15) / 16);       // token tiles with a row
@@ -217,10 +251,10 @@ __global__ __launch_bounds__(NW * 64) void fg_stream_linear_kernel(const uint8_t
             }
             b.ws[0] = sp[lk];
 #pragma unroll
-            for (int t = 0; t < NT; t++) b.x[t].load(xp[t], sx + (int64_t)lk * M + xm[t], k, g);
+            for (int t = 0; t < NT; t++) b.x[t].load(xp[t], sx + (int64_t)lk * M + xm[t], k, lane);
             lk = lk + 1 < k1 ? lk + 1 : lk;
         },
-        [&](Regs& b) { consume<RT, 1, NT, SRC_CODES>(b, 0, tiles, acc); });
+        [&](Regs& b) { consume<RT, 1, NT, SRC_CODES>(b, 0, tiles, source, acc); });
 
 #pragma unroll
     for (int r = 0; r < RT; r++)
@@ -233,17 +267,15 @@ __global__ __launch_bounds__(NW * 64) void fg_stream_linear_kernel(const uint8_t
         const int r = id / NT, t = id % NT;
         const int64_t m = m0 + 16 * t + l16, n = n0 + 16 * r + 4 * g;
         if (m >= M || n >= N) continue;
-        float v[4];
+        v4f v = {0.f, 0.f, 0.f, 0.f}, res = {0.f, 0.f, 0.f, 0.f};
+        if (ep.bias) v = fg_load_four(ep.bias, n, ep.bias_bf16, ep.vector_ok, N - n);
+        if (ep.residual) res = fg_load_four(ep.residual, m * ep.ld_res + n, ep.residual_bf16, ep.vector_ok, N - n);
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            v[q] = 0.0f;
+            float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < NW; w++) v[q] += red[w][id * 4 + q][lane];
-            if (n + q < N) {
-                if (ep.bias) v[q] += fg_load_elem(ep.bias, n + q, ep.bias_bf16);
-                v[q] = fg_act_any(ep.act, v[q]);
-                if (ep.residual) v[q] += fg_load_elem(ep.residual, m * ep.ld_res + n + q, ep.residual_bf16);
-            }
+            for (int w = 0; w < NW; w++) sum += red[w][id * 4 + q][lane];
+            v[q] = fg_act_any(ep.act, sum + v[q]) + res[q];
         }
         if (out_bf16) {
             uint16_t* o = (uint16_t*)y + m * N + n;
@@ -328,7 +360,7 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_up_kernel(FgMoe p, const uint8
     __shared__ int expert;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g = lane >> 4, z = lane_zero();
+    const int l16 = lane & 15, g = lane >> 4, z = lane_zero(), source = operand_source(lane);
     const int nblk = (int)(p.I / (16 * RG));
     const int slot = (int)blockIdx.x / nblk;
     const int64_t n0 = (int64_t)((int)blockIdx.x % nblk) * (16 * RG);
@@ -361,15 +393,20 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_up_kernel(FgMoe p, const uint8
     const uint8_t* wp[RT];
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-        const int64_t n = (r < RG ? 0 : p.I) + n0 + 16 * (r % RG) + l16;
-        wp[r] = p.w1q + ((int64_t)e * 2 * p.I + n) * p.H + 16 * g;
+        const int64_t n = (r < RG ? 0 : p.I) + n0 + 16 * (r % RG) + load_row(lane);
+        wp[r] = p.w1q + ((int64_t)e * 2 * p.I + n) * p.H + 16 * load_group(lane);
     }
     const float* sp[2];
 #pragma unroll
     for (int s = 0; s < 2; s++) sp[s] = p.s1 + ((int64_t)e * 2 * (p.I / 128) + (s * p.I + n0) / 128) * nkb + z;
-    int xt[NT];                          // columns not in use read the first token's row: valid memory, no extra traffic
+    // columns not in use read the first token's row: valid memory, no extra traffic
+    auto token_of = [&](int t) { return ((mask >> t) & 1) ? t : first; };
+    int xt[NT], xr[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) xt[t] = ((mask >> (16 * t + l16)) & 1) ? 16 * t + l16 : first;
+    for (int t = 0; t < NT; t++) {
+        xt[t] = token_of(16 * t + l16);
+        xr[t] = token_of(16 * t + load_row(lane));
+    }
 
     v4f acc[RT][NT];
 #pragma unroll
@@ -391,12 +428,12 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_up_kernel(FgMoe p, const uint8
             b.ws[1] = sp[1][lk];
 #pragma unroll
             for (int t = 0; t < NT; t++) {
-                if constexpr (SRC == SRC_CODES) b.x[t].load(xq + xt[t] * p.H, sx + lk * p.T + xt[t], k, g);
-                else b.x[t].load(p.x + xt[t] * p.ld_x, k, g);
+                if constexpr (SRC == SRC_CODES) b.x[t].load(xq + xr[t] * p.H, sx + lk * p.T + xt[t], k, lane);
+                else b.x[t].load(p.x + xr[t] * p.ld_x, k, lane);
             }
             lk = lk + 1 < k1 ? lk + 1 : lk;
         },
-        [&](Regs& b) { consume<RT, 2, NT, SRC>(b, p.pow2, tiles, acc); });
+        [&](Regs& b) { consume<RT, 2, NT, SRC>(b, p.pow2, tiles, source, acc); });
 
 #pragma unroll
     for (int r = 0; r < RT; r++)
@@ -420,7 +457,8 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_up_kernel(FgMoe p, const uint8
             }
             v[q] = fg_act_any(p.act, gate) * up;
         }
-        *reinterpret_cast<v4f*>(h + ((int64_t)(16 * t + l16) * p.topk + c) * p.I + n0 + 16 * r + 4 * g) = v;
+        const int64_t n = n0 + 16 * r + 4 * g;
+        *reinterpret_cast<v4f*>(h + ((int64_t)(16 * t + l16) * p.topk + c) * p.I + (n & ~127) + hidden_at((int)(n & 127))) = v;
     }
 }
 
@@ -441,7 +479,7 @@ __global__ __launch_bounds__(256) void fg_moe_quant_kernel(FgMoe p, const float*
     float f[8];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const v4f v = ok ? *reinterpret_cast<const v4f*>(h + r * p.I + g * FG_GROUP + lane16 * 8 + 4 * i) : v4f{0.f, 0.f, 0.f, 0.f};
+        const v4f v = ok ? *reinterpret_cast<const v4f*>(h + r * p.I + g * FG_GROUP + hidden_at(lane16 * 8 + 4 * i)) : v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 4; q++) f[4 * i + q] = v[q];
     }
@@ -472,7 +510,7 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
     __shared__ int before[kWords + 1];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int l16 = lane & 15, g = lane >> 4, z = lane_zero();
+    const int l16 = lane & 15, g = lane >> 4, z = lane_zero(), source = operand_source(lane);
     const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
 
     for (int i = tid; i < n_pairs; i += NW * 64) weight[i] = p.weights[i];
@@ -505,10 +543,10 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
     int ls = nkb > 0 ? k0 / nkb : 0, lk = nkb > 0 ? k0 % nkb : 0, left = k1 - k0;
     const uint8_t* wp = nullptr;
     const float* sp = nullptr;
-    int row[NT];
+    int row[NT], lrow[NT];              // rows of the columns' tokens, and of those that this lane loads
     auto enter = [&](int s) {
         const int e = __builtin_amdgcn_readfirstlane(list[s]);
-        wp = p.w2q + ((int64_t)e * p.H + n0 + l16) * p.I + 16 * g;
+        wp = p.w2q + ((int64_t)e * p.H + n0 + load_row(lane)) * p.I + 16 * load_group(lane);
         sp = p.s2 + ((int64_t)e * (p.H / 128) + n0 / 128) * nkb + z;
         // columns not in use read a row that some token of the tile uses, or (no tile) the slot's first
         const int8_t* c = choice + s * (16 * NT);
@@ -524,7 +562,10 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
 #pragma unroll
         for (int t = 0; t < NT; t++) some = some >= 0 ? some : __builtin_amdgcn_readlane(row[t], 0);
 #pragma unroll
-        for (int t = 0; t < NT; t++) row[t] = row[t] >= 0 ? row[t] : some;
+        for (int t = 0; t < NT; t++) {
+            row[t] = row[t] >= 0 ? row[t] : some;
+            lrow[t] = __shfl(row[t], load_row(lane));
+        }
     };
     if (k0 < k1) enter(ls);
     // The consumer's place, with the slot's token tiles.
@@ -547,8 +588,8 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
             b.ws[0] = sp[lk];
 #pragma unroll
             for (int t = 0; t < NT; t++) {
-                if constexpr (SRC == SRC_CODES) b.x[t].load(hq + row[t] * p.I, sh + (int64_t)lk * n_pairs + row[t], k, g);
-                else b.x[t].load(h + row[t] * p.I, k, g);
+                if constexpr (SRC == SRC_CODES) b.x[t].load(hq + lrow[t] * p.I, sh + (int64_t)lk * n_pairs + row[t], k, lane);
+                else b.x[t].load(h + lrow[t] * p.I, k, lane);
             }
             if (left > 1) {
                 left--;
@@ -559,7 +600,7 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
             }
         },
         [&](Regs& b) {
-            consume<RT, 1, NT, SRC>(b, p.pow2, tiles, acc);
+            consume<RT, 1, NT, SRC>(b, p.pow2, tiles, source, acc);
             done++;
             ck++;
             if (ck == nkb || done == k1 - k0) {     // the wave's share of this expert is complete: weigh it
@@ -665,6 +706,7 @@ hipError_t launch_down(const FgMoe& p, const float* h, const uint8_t* hq, const 
     return hipGetLastError();
 }
 
+constexpr int64_t kWideLinear = 4096;  // output columns from which a Linear's workgroups take 32 of them
 constexpr int64_t kFusedTokens = 16;   // up to here the activations are quantized inside the two products
 
 int64_t pad16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
@@ -692,7 +734,7 @@ hipError_t moe_with_codes(const FgMoe& p, uint8_t* ws, const MoeWorkspace& at, i
     hipError_t e = fg_launch_quant_act_cols(p.x, p.T, p.H, p.ld_x, p.pow2, ws + at.xq, (float*)(ws + at.sx), stream);
     if (e != hipSuccess) return e;
     if (p.I > 0) {
-        e = launch_up<2, NT, 4, 2, SRC_CODES>(p, ws + at.xq, (const float*)(ws + at.sx), h, slots, stream);
+        e = launch_up<2, NT, 4, 1, SRC_CODES>(p, ws + at.xq, (const float*)(ws + at.sx), h, slots, stream);
         if (e != hipSuccess) return e;
         const int64_t tiles = p.T * p.topk * (p.I / FG_GROUP);
         hipLaunchKernelGGL(fg_moe_quant_kernel, dim3((unsigned)((tiles + 15) / 16)), dim3(256), 0, stream, p, h, ws + at.hq,
@@ -705,13 +747,27 @@ hipError_t moe_with_codes(const FgMoe& p, uint8_t* ws, const MoeWorkspace& at, i
 
 }  // namespace
 
-bool fg_stream_linear_fits(int64_t M, int64_t N, int64_t K) { return M <= 64; }
+// Estimated time in us of the weight-streaming Linear: 4 us of launch and latency, then a pass over the weights for
+// every 64 rows, the first from HBM and the others from the caches at about the same 5.2 TB/s (3.2 where N leaves 16-row
+// workgroups only), and an LDS exchange that the tokens' operands add to the first pass. Measured: N = 18432,
+// K = 7168: 31 us at M = 16, 48 at 64, 66 at 128, 115 at 256; N = K = 7168: 13.5, 19.5, 29.5, 48.5.
+double fg_stream_linear_us(int64_t M, int64_t N, int64_t K) {
+    const double pass = (double)N * (double)K / (N >= kWideLinear ? 5.2e6 : 3.2e6);
+    return 4.0 + pass * (M <= 16 ? 1.0 : M <= 32 ? 1.2 : (double)((M + 63) / 64) + 0.6);
+}
 
 hipError_t fg_launch_stream_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                    int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, hipStream_t stream) {
-    if (M <= 16) return launch_linear<1, 1, 8, 4>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-    if (M <= 32) return launch_linear<1, 2, 8, 4>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-    return launch_linear<1, 4, 8, 3>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    // 32 output columns a workgroup share each token tile's loads and exchange (N = 7168, K = 18432, M = 16: 28.4 us
+    // against 35.7 with 16), where that leaves workgroups enough; 8 waves split the contraction of the others.
+    if (N >= kWideLinear) {
+        if (M <= 16) return launch_linear<2, 1, 4, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        if (M <= 32) return launch_linear<2, 2, 8, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        return launch_linear<2, 4, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    }
+    if (M <= 16) return launch_linear<1, 1, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    if (M <= 32) return launch_linear<1, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    return launch_linear<1, 4, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
 }
 
 int64_t fg_moe_workspace_bytes(int64_t T, int topk, int64_t H, int64_t I) { return MoeWorkspace(T, topk, H, I).bytes; }
@@ -723,9 +779,12 @@ hipError_t fg_launch_moe_few_tokens(const FgMoe& p, hipStream_t stream) {
     if (p.T > 32) return moe_with_codes<4>(p, ws, at, slots, stream);
     if (p.T > kFusedTokens) return moe_with_codes<2>(p, ws, at, slots, stream);
     float* h = (float*)(ws + at.h);
+    const bool wide_up = slots * (p.I / 32) >= 256, wide_down = p.H >= 32 * 128;
     if (p.I > 0) {
-        const hipError_t e = launch_up<1, 1, 4, 4, SRC_BF16>(p, nullptr, nullptr, h, slots, stream);
+        const hipError_t e = wide_up ? launch_up<2, 1, 4, 2, SRC_BF16>(p, nullptr, nullptr, h, slots, stream)
+                                     : launch_up<1, 1, 8, 1, SRC_BF16>(p, nullptr, nullptr, h, slots, stream);
         if (e != hipSuccess) return e;
     }
-    return launch_down<1, 1, 8, 3, SRC_F32>(p, h, nullptr, nullptr, slots, stream);
+    return wide_down ? launch_down<2, 1, 8, 2, SRC_F32>(p, h, nullptr, nullptr, slots, stream)
+                     : launch_down<1, 1, 8, 1, SRC_F32>(p, h, nullptr, nullptr, slots, stream);
 }

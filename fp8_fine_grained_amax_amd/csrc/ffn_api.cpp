@@ -13,6 +13,7 @@ constexpr int64_t kMaxRows = 1LL << 30;
 constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxExpertDim = 1LL << 20;
 constexpr int64_t kMaxTokens = 64;
+constexpr int64_t kMaxStreamRows = 4096;         // a grid of 64 blocks of rows; its estimate lies far above the tiles' by then
 constexpr int kMaxTopk = 32, kMaxExperts = 2048;
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -44,10 +45,12 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
     if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
         (bias && !aligned(bias, size_of(bias_type))) || (residual && !aligned(residual, size_of(residual_type))))
         return FG_ERR_MISALIGNED;
+    const bool vector_ok = N % 8 == 0 && (!bias || aligned(bias, 16)) &&
+                           (!residual || (ld_res % 8 == 0 && aligned(residual, 16)));
     const FgEpilogue e{bias, residual, ld_res, bias && bias_type == FG_OUT_BF16,
-                       residual && residual_type == FG_OUT_BF16, (int)act};
+                       residual && residual_type == FG_OUT_BF16, (int)act, vector_ok};
     const int bf16 = out == FG_OUT_BF16;
-    if (fg_stream_linear_fits(M, N, K))
+    if (M <= kMaxStreamRows && fg_stream_linear_us(M, N, K) <= fg_gemm_epilogue_us(M, N, K))
         return fg_status_from_hip(fg_launch_stream_linear(xq, sx, wq, sw, M, N, K, e, y, bf16, stream));
     return fg_status_from_hip(
         fg_launch_gemm_fprop_epilogue(xq, sx, wq, sw, M, N, K, e, y, bf16, scales == FG_SCALE_POW2, stream));

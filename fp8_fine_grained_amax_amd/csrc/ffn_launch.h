@@ -11,6 +11,7 @@ struct FgEpilogue {
     const void* residual;
     int64_t ld_res;
     int bias_bf16, residual_bf16, act;
+    int vector_ok;      // bias, residual and output allow 16-byte accesses at every eighth column
 };
 
 struct FgMoe {
@@ -37,8 +38,9 @@ struct FgActBwd {
     float *sdz_cols, *sdz_rows, *sa_rows, *dbias, *partial;
 };
 
-// Longest M that the weight-streaming Linear takes (see few_tokens.hip for both sides of the choice).
-bool fg_stream_linear_fits(int64_t M, int64_t N, int64_t K);
+// Estimated times in us of the two ways to compute a Linear with its epilogue: the smaller one is taken.
+double fg_stream_linear_us(int64_t M, int64_t N, int64_t K);
+double fg_gemm_epilogue_us(int64_t M, int64_t N, int64_t K);
 
 hipError_t fg_launch_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                          int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, int pow2,

@@ -25,8 +25,10 @@ __device__ __forceinline__ float fg_act_value(float z) {
     if constexpr (ACT == FG_ACT_RELU) return __builtin_fmaxf(z, 0.0f);
     if constexpr (ACT == FG_ACT_SILU) return z * fg_sigmoid(z);
     if constexpr (ACT == FG_ACT_GELU_TANH) {
-        float z2;
-        return z * fg_gelu_sigmoid(z, z2);
+        // without the clamp: where z^2 overflows, the sigmoid's argument is infinite and it 0 or 1 all the same.
+        // The constants are those of fg_gelu_sigmoid times -log2(e).
+        const float e = __builtin_amdgcn_exp2f(z * __builtin_fmaf(z * z, -0.102943242f, -2.30220819f));
+        return z * __builtin_amdgcn_rcpf(1.0f + e);
     }
     return z;
 }

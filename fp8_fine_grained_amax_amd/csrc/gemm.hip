@@ -42,8 +42,8 @@
 #include <string.h>
 
 #include "common.h"
+#include "ffn_epilogue.h"
 #include "ffn_launch.h"
-#include "ffn_math.h"
 #include "host_util.h"
 
 namespace {
@@ -74,6 +74,7 @@ struct TileCfg {
 };
 using Cfg12 = TileCfg<4, 3, 64, 64>;   // 256 x 192
 using Cfg8 = TileCfg<2, 4, 128, 64>;   // 256 x 256
+using Cfg4 = TileCfg<2, 2, 64, 64>;    // 128 x 128, the Fprop with epilogue of few tiles (see launch_epilogue())
 
 enum { SB_BLOCK = 0, SB_BLOCK_T = 1, SB_ROW = 2 };
 enum { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
@@ -182,7 +183,7 @@ __device__ __forceinline__ int e8m0_of(float s, uint32_t& bad) {
 // choice because the compiler folds a run-time choice between an ordinary and a non-temporal store of the
 // same value into one ordinary store.
 template <class C, bool B_TRANS, int SBK, int GROUP, bool POW2, int EPI = EPI_STORE, bool STREAM = false>
-__global__ __launch_bounds__(C::NTHREADS, 1) void fg_gemm_kernel(GemmParams p) {
+__global__ __launch_bounds__(C::NTHREADS, C::NW == 4 ? 2 : 1) void fg_gemm_kernel(GemmParams p) {
     constexpr int BM = C::BM, BN = C::BN, NW = C::NW, MSUB = C::MSUB, NSUB = C::NSUB;
     constexpr int WAVE_M = C::WAVE_M, WAVE_N = C::WAVE_N;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(C::NTHREADS, 1) void fg_gemm_kernel(GemmParams p) {
     // grouped) and the FP32-scale grouped Dgrad (1% faster); the other 128x128-block kernels F = 3; the
     // FP32-scale Wgrad spreads them over every row but the last (the loads must be out before the step's
     // hand-over barrier), the power-of-2 Wgrad F = 3 (5% faster than spreading).
-    constexpr int F = C::NW == 12 ? 2
+    constexpr int F = MSUB == 4 ? 2
                     : SBK == SB_ROW ? (POW2 ? 3 : MSUB - 1)
                     : (!POW2 && (!B_TRANS || GROUP == GRP_ROWS)) ? 4 : 3;
     static_assert(F <= MSUB - 1, "the next stage's loads are all issued before the last row's hand-over barrier");
@@ -791,25 +792,10 @@ __global__ __launch_bounds__(C::NTHREADS, 1) void fg_gemm_kernel(GemmParams p) {
         return;
     }
     if constexpr (EPI == EPI_ACT) {
-        // act(acc + bias) + residual in the MFMA layout, on the fp32 sums; the store below rounds once.
-#pragma unroll
-        for (int j = 0; j < NSUB; j++) {
-            const int64_t n = wave_n0 + j * 16 + lcol4;
-            float b[4];
-#pragma unroll
-            for (int r = 0; r < 4; r++) b[r] = p.ep.bias && n + r < N ? fg_load_elem(p.ep.bias, n + r, p.ep.bias_bf16) : 0.0f;
-#pragma unroll
-            for (int i = 0; i < MSUB; i++) {
-                const int64_t m = m0 + wm * WAVE_M + i * 16 + lrow;
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    float v = fg_act_any(p.ep.act, acc[i][j][r] + b[r]);
-                    if (p.ep.residual && m < m_end && n + r < N)
-                        v += fg_load_elem(p.ep.residual, m * p.ep.ld_res + n + r, p.ep.residual_bf16);
-                    acc[i][j][r] = v;
-                }
-            }
-        }
+        static_assert(NW * 32 * WAVE_N * 4 <= C::LDS_BYTES, "the staging regions fit the stages");
+        __syncthreads();                         // every wave's staging loads and LDS reads are done
+        fg_store_epilogue<WAVE_N>(p.ep, acc, smem + wave * (32 * WAVE_N * 4), lane, m0 + wm * WAVE_M, m_end, wave_n0, N, outp, p.out_bf16);
+        return;
     }
     if constexpr (NW == 8 && WAVE_M == 128 && WAVE_N == 64 && C::LDS_BYTES >= NW * 64 * 256) {
         // FP32 output through LDS. In the MFMA layout one 16-byte store per lane writes 16 rows x 64 B, and
@@ -955,7 +941,7 @@ struct WideCfg {
     static_assert(SLICES_A <= NW, "one scale slice per wave");
 };
 
-template <bool POW2, bool STREAM>
+template <bool POW2, bool STREAM, int EPI>
 __global__ __launch_bounds__(WideCfg::NTHREADS, 1) void fg_gemm_wide_kernel(GemmParams p) {
     using C = WideCfg;
     constexpr int BM = C::BM, BN = C::BN, NW = C::NW, MSUB = C::MSUB, NSUB = C::NSUB;
@@ -1192,6 +1178,12 @@ __global__ __launch_bounds__(WideCfg::NTHREADS, 1) void fg_gemm_wide_kernel(Gemm
     }
 
     // ---------------- epilogue ----------------
+    if constexpr (EPI == EPI_ACT) {
+        static_assert(C::OUT_REGION >= 32 * WAVE_N * 4, "the staging regions hold 32 rows");
+        __syncthreads();
+        fg_store_epilogue<WAVE_N>(p.ep, acc, smem + wave * C::OUT_REGION, lane, m0 + wm * WAVE_M, M, wave_n0, N, p.out, p.out_bf16);
+        return;
+    }
     // A wave whose 144 columns lie inside the output re-lays its tile in a private LDS region (64 rows of
     // 288 B for BF16; FP32 in two halves of 32 rows of 576 B) and stores it as contiguous 16-byte chunks:
     // the region is dense, so chunk f of it is row f / (chunks per row), and one store instruction writes
@@ -1375,14 +1367,45 @@ bool use_wide(const GemmParams& p) {
     return rw * WideCfg::BN < r8 * Cfg8::BN;
 }
 
-template <bool POW2, bool STREAM>
+template <bool POW2, bool STREAM, int EPI = EPI_STORE>
 hipError_t launch_wide(const GemmParams& p, unsigned grid, hipStream_t stream) {
-    auto kern = fg_gemm_wide_kernel<POW2, STREAM>;
+    auto kern = fg_gemm_wide_kernel<POW2, STREAM, EPI>;
     static std::atomic<uint64_t> lds_limit_set{0};
     const hipError_t e = fg_set_lds_limit_once((const void*)kern, WideCfg::LDS_BYTES, lds_limit_set);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kern, dim3(grid), dim3(WideCfg::NTHREADS), WideCfg::LDS_BYTES, stream, p);
     return hipGetLastError();
+}
+
+// The Fprop with its epilogue picks among the Fprop's shapes as fg_launch_gemm_fprop does, and takes 128 x 128 tiles
+// (two workgroups a CU) where they are estimated to end sooner: with few tiles a K step takes each shape the time its
+// loads need, and the smaller shape's come back sooner and leave fewer CUs without a tile. Time of a K step in us
+// with FP32 scales, from launches of less than one round (M = 16 to 768, N, K = 1024 to 18432, 80 problems).
+constexpr double kStep4 = 1.07, kStep4Full = 1.28, kStep12 = 1.55, kStep8 = 1.65, kStepWide = 1.85;
+
+int64_t rounds(int64_t tiles, int64_t per_round) { return (tiles + per_round - 1) / per_round; }
+
+double tile4_us(const GemmParams& p) {
+    const int64_t cus = fg_device_cus(), tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
+    return (double)(p.K / BK) * (tiles <= cus ? kStep4 : kStep4Full * (double)rounds(tiles, 2 * cus));
+}
+double large_tile_us(const GemmParams& p) {
+    const int64_t cus = fg_device_cus(), m_tiles = (p.M + 255) / 256;
+    const bool wide = use_wide(p), cfg8 = use_cfg8(p, GRP_NONE);
+    const int64_t bn = wide ? WideCfg::BN : cfg8 ? Cfg8::BN : Cfg12::BN;
+    return (double)(p.K / BK) * (wide ? kStepWide : cfg8 ? kStep8 : kStep12) * (double)rounds(m_tiles * ((p.N + bn - 1) / bn), cus);
+}
+
+template <bool POW2>
+hipError_t launch_epilogue(const GemmParams& p, hipStream_t stream) {
+    if (!getenv("FG_GEMM_TILE") && tile4_us(p) < large_tile_us(p))
+        return launch_one<Cfg4, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg4>(p, GRP_NONE), stream);
+    if (use_wide(p)) {
+        const unsigned grid = (unsigned)(((p.M + WideCfg::BM - 1) / WideCfg::BM) * ((p.N + WideCfg::BN - 1) / WideCfg::BN));
+        return launch_wide<POW2, false, EPI_ACT>(p, grid, stream);
+    }
+    if (use_cfg8(p, GRP_NONE)) return launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg8>(p, GRP_NONE), stream);
+    return launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg12>(p, GRP_NONE), stream);
 }
 
 }  // namespace
@@ -1402,20 +1425,21 @@ hipError_t fg_launch_gemm_fprop(const uint8_t* xq, const float* sx, const uint8_
     return launch<false, SB_BLOCK, GRP_NONE>(p, pow2, stream);
 }
 
+double fg_gemm_epilogue_us(int64_t M, int64_t N, int64_t K) {
+    if (getenv("FG_GEMM_TILE")) return 0.0;      // a forced tile: these kernels
+    GemmParams p{};
+    p.M = M; p.N = N; p.K = K;
+    const double small = tile4_us(p), large = large_tile_us(p);
+    return 4.0 + (small < large ? small : large);
+}
+
 hipError_t fg_launch_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                          int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, int pow2,
                                          hipStream_t stream) {
     GemmParams p{};
     p.a = xq; p.sa = sx; p.sa_ld = M; p.b = wq; p.sb = sw;
     p.M = M; p.N = N; p.K = K; p.out = y; p.out_bf16 = out_bf16; p.ep = e;
-    if (use_cfg8(p, GRP_NONE)) {
-        const unsigned grid = grid_for<Cfg8>(p, GRP_NONE);
-        return pow2 ? launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, true, EPI_ACT>(p, grid, stream)
-                    : launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, false, EPI_ACT>(p, grid, stream);
-    }
-    const unsigned grid = grid_for<Cfg12>(p, GRP_NONE);
-    return pow2 ? launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, true, EPI_ACT>(p, grid, stream)
-                : launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, false, EPI_ACT>(p, grid, stream);
+    return pow2 ? launch_epilogue<true>(p, stream) : launch_epilogue<false>(p, stream);
 }
 
 hipError_t fg_launch_gemm_dgrad(const uint8_t* dyq, const float* sdy, const uint8_t* wq, const float* sw, int64_t M,

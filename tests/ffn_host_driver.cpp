@@ -16,7 +16,8 @@ hipError_t hit() {
 }
 }  // namespace
 
-bool fg_stream_linear_fits(int64_t M, int64_t, int64_t) { return M <= 64; }
+double fg_stream_linear_us(int64_t M, int64_t, int64_t) { return (double)M; }
+double fg_gemm_epilogue_us(int64_t, int64_t, int64_t) { return 64.0; }
 hipError_t fg_launch_gemm_fprop_epilogue(const uint8_t*, const float*, const uint8_t*, const float*, int64_t, int64_t, int64_t,
                                          const FgEpilogue&, void*, int, int, hipStream_t) { return hit(); }
 hipError_t fg_launch_stream_linear(const uint8_t*, const float*, const uint8_t*, const float*, int64_t, int64_t, int64_t,

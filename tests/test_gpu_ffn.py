@@ -78,6 +78,31 @@ def test_linear_epilogues(M, N, kind, types):
     check_linear(ops, y, kind, bias, residual)
 
 
+@pytest.mark.parametrize("M,N,types", [(300, 576, "fff"), (300, 580, "bbf"), (257, 333, "bfb"), (64, 1160, "ffb")])
+@pytest.mark.parametrize("kind", ["gelu", "relu"])
+@pytest.mark.parametrize("tile", ["256x192", "256x256", "256x288"])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_linear_epilogue_on_every_tile(M, N, types, kind, tile, pow2, monkeypatch):
+    monkeypatch.setenv("FG_GEMM_TILE", tile)
+    t = {"f": torch.float32, "b": torch.bfloat16}
+    ops = linear_case(M + N, M, N, 384, pow2)
+    bias, residual = rand(1, N, dtype=t[types[0]]), rand(2, M, N, dtype=t[types[1]])
+    y = torch.full((M, N), float("nan"), dtype=t[types[2]], device=device())
+    fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=act_code(kind), residual=residual, y=y, pow2=pow2)
+    check_linear(ops, y, kind, bias, residual)
+
+
+@pytest.mark.parametrize("M,N,K", [(640, 4096, 1024), (1000, 3000, 512), (2048, 2056, 256)])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_linear_on_small_tiles(M, N, K, pow2):
+    """Sizes whose launches take the 128x128 tiles."""
+    ops = linear_case(M, M, N, K, pow2)
+    bias, residual = rand(1, N), rand(2, M, N)
+    y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=device())
+    fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_SILU, residual=residual, y=y, pow2=pow2)
+    check_linear(ops, y, "silu", bias, residual)
+
+
 @pytest.mark.parametrize("M", [1, 16, 64, 65, 256])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_linear_residual_in_place(M, dtype):
@@ -97,10 +122,12 @@ def test_linear_empty_contraction(M):
     check_linear(ops, y, "gelu", bias, residual)
 
 
-@pytest.mark.parametrize("M,N", [(100, 384), (300, 520), (512, 1024)])
+@pytest.mark.parametrize("M,N", [(100, 384), (300, 520), (512, 1024), (257, 777)])
 @pytest.mark.parametrize("pow2", [False, True])
-def test_linear_without_epilogue_is_the_fprop(M, N, pow2):
+@pytest.mark.parametrize("tile", ["256x192", "256x256", "256x288"])
+def test_linear_without_epilogue_is_the_fprop(M, N, pow2, tile, monkeypatch):
     """On the GEMM tiles the sums are the Fprop's own, bit for bit."""
+    monkeypatch.setenv("FG_GEMM_TILE", tile)
     ops = linear_case(9, M, N, 512, pow2)
     for dtype in (torch.float32, torch.bfloat16):
         assert torch.equal(fg.fg_fp8_gemm_fprop_epilogue(*ops, out_dtype=dtype, pow2=pow2),
