@@ -114,21 +114,18 @@ __device__ __forceinline__ v8i act_operand(const ActRegs<SRC>& r, int pow2, int 
 #pragma unroll
         for (int i = 0; i < 32; i++) m = __builtin_fmaxf(m, __builtin_fabsf(f[i]));
         const float own = fg_scale_from_amax(quad_max(m), pow2);
-        // one form for both scale modes: a power-of-2 scale's first quotient is exact and its correction 0
-        fg_divisor d = fg_make_divisor(own, pow2);
-        if (__builtin_amdgcn_ballot_w64(fg_small_scale(own)) != 0 && fg_small_scale(own)) {
-            d = fg_divisor_shifted(d);
+        const fg_divisor d = fg_divisor_of(own);
+        const bool small = fg_any_small(own);
+        v4i c[2];
+        if (!small) {
 #pragma unroll
-            for (int i = 0; i < 32; i++) f[i] *= 0x1p64f;
-        }
-        v4i lo, hi;
+            for (int i = 0; i < 8; i++) c[i >> 2][i & 3] = (int)fg_quant4<false>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], d);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            lo[i] = (int)fg_quant4<FG_Q_FAST>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], d);
-            hi[i] = (int)fg_quant4<FG_Q_FAST>(f[16 + 4 * i], f[17 + 4 * i], f[18 + 4 * i], f[19 + 4 * i], d);
+            for (int i = 0; i < 8; i++) c[i >> 2][i & 3] = (int)fg_quant4<true>(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3], d);
         }
         s = __int_as_float(__builtin_amdgcn_ds_bpermute(source, __float_as_int(own)));
-        return to_operand(lo, hi, source);
+        return to_operand(c[0], c[1], source);
     }
 }
 
@@ -532,9 +529,9 @@ __global__ __launch_bounds__(256) void fg_moe_quant_kernel(FgMoe p, const float*
 #pragma unroll
     for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, __builtin_fabsf(f[i]));
     const float s = fg_scale_from_amax(fg_row16_max(m), p.pow2);
-    const fg_divisor d = fg_make_divisor(s, p.pow2);
-    const int form = fg_quot_form(s, p.pow2);
-    const uint2 c = make_uint2(fg_quant4_any(form, f[0], f[1], f[2], f[3], d), fg_quant4_any(form, f[4], f[5], f[6], f[7], d));
+    const fg_divisor d = fg_divisor_of(s);
+    const bool small = fg_any_small(s);
+    const uint2 c = make_uint2(fg_quant4(f[0], f[1], f[2], f[3], d, small), fg_quant4(f[4], f[5], f[6], f[7], d, small));
     if (!ok) return;
     *reinterpret_cast<uint2*>(hq + r * p.I + g * FG_GROUP + lane16 * 8) = c;
     if (lane16 == 0) sh[g * rows + r] = s;

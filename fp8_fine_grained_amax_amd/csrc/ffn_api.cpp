@@ -8,8 +8,8 @@ namespace {
 
 constexpr int64_t kMaxGrid = 2147483647LL;
 constexpr int64_t kMaxContraction = 1LL << 24;   // as in the other GEMMs: 32-bit operand offsets
-constexpr int64_t kMaxCols = 1LL << 30;          // row widths whose products with element sizes stay far below 2^63
-constexpr int64_t kMaxRows = 1LL << 30;
+constexpr int64_t kMaxCols = 1LL << 23;          // 32-bit offsets inside a 128-row block of up to 2 F codes or F fp32 values
+constexpr int64_t kMaxRows = 1LL << 25;          // and inside a 128-column block of a tiling along the rows
 constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxExpertDim = 1LL << 20;
 constexpr int64_t kMaxTokens = 64;
@@ -82,7 +82,7 @@ fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* 
     if (rows < 0 || F < 0 || ld_da < F || !valid_mode(mode) || !valid_act(act) || !valid_type(da_type) ||
         (gated != 0 && gated != 1) || workspace_bytes < 0)
         return FG_ERR_INVALID_ARG;
-    if (F > kMaxCols || rows > kMaxRows || ld_da > kMaxStride) return FG_ERR_UNSUPPORTED_SHAPE;
+    if (F > kMaxCols || rows > kMaxRows || ld_da > kMaxCols) return FG_ERR_UNSUPPORTED_SHAPE;
     if (F == 0 || (rows == 0 && !dbias)) return FG_OK;
     if (!dzq_rows != !sdz_rows || !aq_rows != !sa_rows) return FG_ERR_INVALID_ARG;
     if (rows > 0 && (!zq || !sz || !da || !dzq_cols || !sdz_cols)) return FG_ERR_INVALID_ARG;

@@ -64,59 +64,82 @@ __device__ __forceinline__ float fg_act_any(int act, float z) {
     }
 }
 
-// Scale of a group of fp32 values from their max-abs: as fg_scale_from_amax_bits, whose corrected product
-// equals the correctly rounded amax / 448 while its remainder is exact; below 2^-80 the division itself.
-__device__ __forceinline__ float fg_scale_from_amax(float amax, int pow2) {
+// Scales of N groups of fp32 values from their max-abs: as fg_scale_from_amax_bits, whose corrected product equals
+// the correctly rounded amax / 448 while its remainder is exact; below 2^-80 (rare: one branch for all the groups) the
+// division itself. Call with the whole wave active.
+template <int N>
+__device__ __forceinline__ void fg_scales_from_amax(const float (&amax)[N], int pow2, float (&s)[N]) {
     const float c = 0x1.24924ap-9f;                     // RN(1/448)
-    const float q0 = amax * c;
-    float s = __builtin_fmaf(__builtin_fmaf(-q0, 448.0f, amax), c, q0);
-    if (amax < 0x1p-80f) s = amax / 448.0f;
-    s = s < 1.17549435e-38f ? 1.17549435e-38f : s;
-    if (pow2) {
-        const uint32_t u = __float_as_uint(s);
-        s = __uint_as_float((u & 0x007FFFFFu) ? (u & 0x7F800000u) + 0x00800000u : u);
+    float least = amax[0];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const float q0 = amax[i] * c;
+        s[i] = __builtin_fmaf(__builtin_fmaf(-q0, 448.0f, amax[i]), c, q0);
+        least = __builtin_fminf(least, amax[i]);
     }
-    return amax == 0.0f ? 1.0f : s;
+    if (__builtin_amdgcn_ballot_w64(least < 0x1p-80f) != 0) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const float q = amax[i] / 448.0f;
+            if (amax[i] < 0x1p-80f) s[i] = amax[i] == 0.0f ? 1.0f : q < 1.17549435e-38f ? 1.17549435e-38f : q;
+        }
+    }
+    if (pow2) {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const uint32_t u = __float_as_uint(s[i]);
+            s[i] = __uint_as_float((u & 0x007FFFFFu) ? (u & 0x7F800000u) + 0x00800000u : u);
+        }
+    }
+}
+__device__ __forceinline__ float fg_scale_from_amax(float amax, int pow2) {
+    const float m[1] = {amax};
+    float s[1];
+    fg_scales_from_amax(m, pow2, s);
+    return s[0];
 }
 
-// Quotient forms for fp32 values, as in common.h: the remainder of the corrected quotient has up to 48 bits
-// here, so it is exact for scales from 2^-80 on (quotients that encode to a code other than 0 are at least
-// 2^-10), and smaller scales are moved up by 2^64 with their values.
+// The divisor of a group whose values are quantized from fp32: the reciprocal refined once is within a unit in the
+// last place, and the corrected quotient (fg_quot_arg) is then off by at most 2^-22 of one before its rounding. A
+// quotient that is a tie between two codes is exact, and a power-of-2 scale's too, so one form serves both modes.
+// The remainder has up to 48 bits here: it is exact for scales from 2^-80 on (quotients that encode to a code other
+// than 0 are at least 2^-10), and smaller scales are moved up by 2^64 with their values.
+__device__ __forceinline__ fg_divisor fg_divisor_of(float s) {
+    const float r = __builtin_amdgcn_rcpf(s);
+    return fg_divisor{s, __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r)};
+}
 __device__ __forceinline__ bool fg_small_scale(float s) { return s < 0x1p-80f; }
 
-// The form of a wave whose lanes hold the scales s: uniform. Call with the whole wave active.
-__device__ __forceinline__ int fg_quot_form(float s, int pow2) {
-    if (pow2) return FG_Q_POW2;
-    return __builtin_amdgcn_ballot_w64(fg_small_scale(s)) == 0 ? FG_Q_FAST : FG_Q_TINY;
-}
-
-// Four fp32 values by the divisors of their groups -> four E4M3 codes in a dword. FORM is the wave's; under
-// FG_Q_TINY each lane takes the form of its own scale.
-template <int FORM>
+// Four fp32 values by the divisor of their group -> four E4M3 codes in a dword. SMALL: the scale may be below 2^-80.
+template <bool SMALL>
 __device__ __forceinline__ uint32_t fg_quant4(float a, float b, float c, float e, const fg_divisor& d) {
-    if constexpr (FORM == FG_Q_TINY) {
-        if (!fg_small_scale(d.s)) return fg_quant4<FG_Q_FAST>(a, b, c, e, d);
-        const fg_divisor m = fg_divisor_shifted(d);
-        return fg_cvt2q<FG_Q_TINY, true>(c, e, m, fg_cvt2q<FG_Q_TINY, false>(a, b, m, 0));
-    } else {
-        return fg_cvt2q<FORM, true>(c, e, d, fg_cvt2q<FORM, false>(a, b, d, 0));
-    }
+    const uint32_t q = fg_cvt2q<FG_Q_FAST, true>(c, e, d, fg_cvt2q<FG_Q_FAST, false>(a, b, d, 0));
+    if constexpr (!SMALL) return q;
+    const fg_divisor m = fg_divisor_shifted(d);
+    const uint32_t t = fg_cvt2q<FG_Q_TINY, true>(c, e, m, fg_cvt2q<FG_Q_TINY, false>(a, b, m, 0));
+    return fg_small_scale(d.s) ? t : q;
 }
-__device__ __forceinline__ uint32_t fg_quant4_any(int form, float a, float b, float c, float e, const fg_divisor& d) {
-    if (form == FG_Q_POW2) return fg_quant4<FG_Q_POW2>(a, b, c, e, d);
-    if (form == FG_Q_FAST) return fg_quant4<FG_Q_FAST>(a, b, c, e, d);
-    return fg_quant4<FG_Q_TINY>(a, b, c, e, d);
+// `small` is uniform over the wave.
+__device__ __forceinline__ uint32_t fg_quant4(float a, float b, float c, float e, const fg_divisor& d, bool small) {
+    return small ? fg_quant4<true>(a, b, c, e, d) : fg_quant4<false>(a, b, c, e, d);
 }
+__device__ __forceinline__ bool fg_any_small(float s) { return __builtin_amdgcn_ballot_w64(fg_small_scale(s)) != 0; }
 
-// Max across the 16 lanes of a DPP row.
-__device__ __forceinline__ float fg_row16_max(float v) {
-#define FG_STEP(ctrl) v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false)))
-    FG_STEP(0x128);
-    FG_STEP(0x124);
-    FG_STEP(0x4E);
-    FG_STEP(0xB1);
+// Max across the 16 lanes of a DPP row, of values that are not negative: their bits order like them, and the integer
+// max takes its DPP operand as it is (the float one would first quiet NaNs, an instruction more a step).
+__device__ __forceinline__ float fg_row16_max(float f) {
+    uint32_t v = __float_as_uint(f);
+#define FG_STEP(ctrl)                                                                             \
+    {                                                                                             \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, false); \
+        v = o > v ? o : v;                                                                        \
+    }
+    FG_STEP(0x128)
+    FG_STEP(0x124)
+    FG_STEP(0x4E)
+    FG_STEP(0xB1)
 #undef FG_STEP
-    return v;
+    return __uint_as_float(v);
 }
 
 __device__ __forceinline__ uint32_t fg_bf16_bits(float f) { return (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)f); }

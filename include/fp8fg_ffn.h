@@ -47,7 +47,7 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
  *       factor: a = act(gate) * up).
  *   zq  u8 [rows][W], sz f32 [W/128][rows]: fg_quantize_act_1x128(z, FG_ALONG_COLS, mode), bit for bit.
  *   aq  u8 [rows][F], sa f32 [F/128][rows]: a in the same tiling, the next Linear's input.
- *   F % 128 == 0, any rows. z, zq, aq 16-byte aligned; ld_z % 8 == 0; sz, sa 4-byte aligned.
+ *   F % 128 == 0, F <= 2^23, rows <= 2^25. z, zq, aq 16-byte aligned; ld_z % 8 == 0; sz, sa 4-byte aligned.
  *   rows == 0 or F == 0 is a no-op. */
 fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t ld_z, fg_act act, int gated,
                                 fg_scale_mode mode, uint8_t* zq, float* sz, uint8_t* aq, float* sa, hipStream_t stream);
@@ -66,7 +66,8 @@ fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t 
  *   workspace  fg_act_checkpoint_bwd_workspace(rows, F, gated) bytes, read and written only with dbias; may be NULL
  *            where that is 0 or dbias is NULL. 4-byte aligned. One call's contents mean nothing to the next; calls
  *            that may run at the same time need workspaces of their own.
- *   F % 128 == 0; rows % 128 == 0 where a tiling along the rows is asked for, any rows otherwise. zq, da, dzq_cols,
+ *   F % 128 == 0; rows % 128 == 0 where a tiling along the rows is asked for, any rows otherwise; F and ld_da at most
+ *   2^23, rows at most 2^25. zq, da, dzq_cols,
  *   dzq_rows, aq_rows 16-byte aligned, ld_da a multiple of 16 bytes; the fp32 outputs and sz 4-byte aligned.
  *   rows == 0 or F == 0: no-op, but for dbias, which becomes 0. */
 int64_t fg_act_checkpoint_bwd_workspace(int64_t rows, int64_t F, int gated);

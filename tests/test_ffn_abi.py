@@ -53,7 +53,8 @@ def test_act_forward_rejections(L):
     assert f(rows=-1) == INVALID and f(F=-128) == INVALID and f(act=7) == INVALID and f(gated=2) == INVALID
     assert f(mode=3) == INVALID and f(ld=128) == INVALID and f(z=None) == INVALID and f(sa=None) == INVALID
     assert f(F=192, ld=384) == SHAPE and f(F=1 << 31, ld=1 << 33) == SHAPE and f(rows=1 << 31) == SHAPE
-    assert f(rows=1 << 30, F=1 << 20, ld=1 << 22) == SHAPE                          # more workgroups than a launch has
+    assert f(F=(1 << 23) + 128, ld=1 << 25) == SHAPE and f(rows=(1 << 25) + 1) == SHAPE
+    assert f(rows=1 << 25, F=1 << 23, ld=1 << 25) == SHAPE                          # more workgroups than a launch has
     assert f(z=ODD) == MISALIGNED and f(ld=260) == MISALIGNED and f(zq=ODD) == MISALIGNED and f(sz=B + 2) == MISALIGNED
     assert f(rows=0, z=None, zq=None) == OK and f(F=0, ld=0, z=None) == OK
 
@@ -68,6 +69,7 @@ def test_act_backward_rejections(L):
     assert f(qr=None) == INVALID and f(sr=None) == INVALID and f(ar=None) == INVALID and f(sa=None) == INVALID   # halves of a pair
     assert f(ws=None) == INVALID and f(nws=2 * 256 * 4 - 1) == INVALID
     assert f(rows=200) == SHAPE and f(F=100) == SHAPE and f(F=1 << 31, ld=1 << 31) == SHAPE and f(rows=1 << 31) == SHAPE
+    assert f(F=(1 << 23) + 128, ld=1 << 23) == INVALID and f(ld=(1 << 23) + 4) == SHAPE and f(rows=(1 << 25) + 128) == SHAPE
     assert f(rows=200, qr=None, sr=None) == SHAPE                                   # a along the rows alone
     assert f(zq=ODD) == MISALIGNED and f(ld=130) == MISALIGNED and f(dt=1, ld=132) == MISALIGNED and f(db=B + 2) == MISALIGNED
     assert f(rows=0, zq=None, sz=None, da=None, qc=None, sc=None, db=None) == OK and f(F=0, ld=0, zq=None) == OK
