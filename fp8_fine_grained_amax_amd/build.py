@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8fg.so")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "per_tensor.hip", "e5m6.hip", "limited_accum.hip", "act_checkpoint.hip",
-           "few_tokens.hip"]
+           "stream_linear.hip", "moe_few_tokens.hip"]
 HOST_SOURCES = ["ffn_api.cpp"]          # argument checks only: no device code
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -96,8 +96,12 @@ def test_workspace_sizes(L):
     assert w(-1, 256, 0) == 0 and w(1 << 40, 256, 0) == 0
     m = L.fg_moe_few_tokens_workspace
     assert m(4, 2, 256, 128) == 4 * 2 * 128 * 4 and m(0, 2, 256, 128) == 0 and m(65, 2, 256, 128) == 0
+    # more tokens: the plan and the activations' codes besides the hidden values; never less for more of anything
     rows = 64 * 8
-    assert m(64, 8, 7168, 2048) == rows * 2048 * 5 + 64 * 7168 + 56 * 64 * 4 + 16 * rows * 4
+    assert m(64, 8, 7168, 2048) > rows * 2048 * 5 + 64 * 7168
+    for a, b in (((16, 8, 1024, 512), (17, 8, 1024, 512)), ((17, 2, 256, 128), (64, 2, 256, 128)), ((64, 2, 256, 128), (64, 32, 256, 128)),
+                 ((64, 8, 2048, 1024), (64, 8, 2048, 2048))):
+        assert m(*a) < m(*b), (a, b)
 
 
 def test_binding_refuses_cpu_tensors():

@@ -440,6 +440,32 @@ def test_moe_is_the_training_layer():
     assert float((y.double() - want).norm() / want.norm()) <= 2.0 ** -5
 
 
+@pytest.mark.parametrize("T,E,topk,H,I", [(9, 48, 6, 1024, 512), (48, 32, 6, 512, 1024), (64, 40, 8, 2048, 256), (16, 16, 16, 384, 1152)])
+def test_moe_split_down_projection(T, E, topk, H, I):
+    """Narrow models with many experts: the down-projection's column blocks are shared between workgroups."""
+    w = experts(E, E, H, I)
+    x = rand(T, T, H)
+    ids, weights = routing(T + E, T, topk, E, E)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = fg.fg_moe_few_tokens(x, ids, weights, *w, out_dtype=dtype)
+        check_moe(y, (x, ids, weights, *w), "silu", False)
+
+
+def test_moe_every_tile_count():
+    """Experts with 0, 1, 15, 16, 17, 32, 33, 48, 49 and 64 tokens in one call."""
+    counts = [0, 1, 15, 16, 17, 32, 33, 48, 49, 64]
+    T, E, H, I = 64, len(counts), 256, 256
+    ids = torch.full((T, E), -1, dtype=torch.int32)
+    g = torch.Generator().manual_seed(1)
+    for e, n in enumerate(counts):
+        ids[torch.randperm(T, generator=g)[:n], e] = e
+    ids = ids[:, torch.randperm(E, generator=g)].to(device())
+    weights = torch.rand(T, E, generator=g).to(device())
+    w = experts(3, E, H, I)
+    x = rand(4, T, H)
+    check_moe(fg.fg_moe_few_tokens(x, ids, weights, *w, out_dtype=torch.float32), (x, ids, weights, *w), "silu", False)
+
+
 def test_moe_empty():
     w = experts(1, 2, 256, 128)
     dev = device()
