@@ -55,7 +55,38 @@ def build(verbose: bool = False, extra=()) -> str:
         sys.stderr.write(r.stderr + "\n")
         raise RuntimeError("the built library does not load: " + r.stderr.strip().splitlines()[-1])
     os.replace(LIB + ".tmp", LIB)
+    build_ffn_module(verbose)
     return LIB
+
+
+FFN_MODULE = os.path.join(HERE, "_ffn.so")
+
+
+def build_ffn_module(verbose: bool = False) -> str:
+    """_ffn.so: the compiled Python binding of the feed-forward operators (csrc/ffn_binding.cpp), against the installed
+    torch's headers and libraries and libfp8fg.so in this package directory."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(base, "include"),
+           "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
+           os.path.join(CSRC, "ffn_binding.cpp"), "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-ltorch_hip", "-lc10", "-lc10_hip", "-L", HERE, "-lfp8fg", "-Wl,-rpath,$ORIGIN", "-o", FFN_MODULE + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stderr + "\n")
+        raise RuntimeError("g++ failed on csrc/ffn_binding.cpp")
+    r = subprocess.run([sys.executable, "-c", "import ctypes, sys, torch; ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_LOCAL)",
+                        FFN_MODULE + ".tmp"], capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stderr + "\n")
+        raise RuntimeError("the built binding does not load: " + r.stderr.strip().splitlines()[-1])
+    os.replace(FFN_MODULE + ".tmp", FFN_MODULE)
+    return FFN_MODULE
 
 
 C_CONSUMER = os.path.join(ROOT, "tests", "c_consumer")
