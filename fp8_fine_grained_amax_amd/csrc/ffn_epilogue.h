@@ -112,17 +112,39 @@ __device__ __forceinline__ void fg_store_epilogue(const FgEpilogue& ep, const v4
                 }
             }
         } else {
-#pragma unroll 4
-            for (int k = 0; k < 32 * WAVE_N / 64; k++) {
-                const int f = 64 * k + lane, r = f / WAVE_N, c = f % WAVE_N;
-                const int64_t row = m_h + r, col = n + c;
-                if (row >= m_end || col >= N) continue;
-                float v = *reinterpret_cast<const float*>(chunk(r, c >> 2) + 4 * (c & 3));
-                const float res = ep.residual ? fg_load_elem(ep.residual, row * ep.ld_res + col, ep.residual_bf16) : 0.0f;
-                if (ep.bias) v += fg_load_elem(ep.bias, col, ep.bias_bf16);
-                v = fg_act_any(ep.act, v) + res;
-                if (out_bf16) ((uint16_t*)out)[row * N + col] = (uint16_t)fg_bf16_bits(v);
-                else ((float*)out)[row * N + col] = v;
+#pragma unroll 1
+            for (int k0 = 0; k0 < 32 * WAVE_N / 64; k0 += 8) {
+                uint32_t res[8], bias[8];                           // as loaded, a group's loads together (in bounds)
+                auto at = [&](int k, int64_t& row, int64_t& col) {
+                    const int f = 64 * (k0 + k) + lane;
+                    row = m_h + f / WAVE_N < m_end ? m_h + f / WAVE_N : m_end - 1;
+                    col = n + f % WAVE_N < N ? n + f % WAVE_N : N - 1;
+                };
+                auto load = [&](uint32_t (&raw)[8], const void* from, int64_t ld, int bf16) {
+                    int64_t row, col;
+                    if (!from) return;
+                    if (bf16) {
+#pragma unroll
+                        for (int k = 0; k < 8; k++) at(k, row, col), raw[k] = ((const uint16_t*)from)[row * ld + col];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; k++) at(k, row, col), raw[k] = ((const uint32_t*)from)[row * ld + col];
+                    }
+                };
+                load(res, ep.residual, ep.ld_res, ep.residual_bf16);
+                load(bias, ep.bias, 0, ep.bias_bf16);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const int f = 64 * (k0 + k) + lane, r = f / WAVE_N, c = f % WAVE_N;
+                    const int64_t row = m_h + r, col = n + c;
+                    if (row >= m_end || col >= N) continue;
+                    float v = *reinterpret_cast<const float*>(chunk(r, c >> 2) + 4 * (c & 3));
+                    if (ep.bias) v += __uint_as_float(ep.bias_bf16 ? bias[k] << 16 : bias[k]);
+                    v = fg_act_any(ep.act, v);
+                    if (ep.residual) v += __uint_as_float(ep.residual_bf16 ? res[k] << 16 : res[k]);
+                    if (out_bf16) ((uint16_t*)out)[row * N + col] = (uint16_t)fg_bf16_bits(v);
+                    else ((float*)out)[row * N + col] = v;
+                }
             }
         }
     }

@@ -41,6 +41,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "common.h"
 #include "ffn_epilogue.h"
 #include "ffn_launch.h"
@@ -74,7 +76,6 @@ struct TileCfg {
 };
 using Cfg12 = TileCfg<4, 3, 64, 64>;   // 256 x 192
 using Cfg8 = TileCfg<2, 4, 128, 64>;   // 256 x 256
-using Cfg4 = TileCfg<2, 2, 64, 64>;    // 128 x 128, the Fprop with epilogue of few tiles (see launch_epilogue())
 
 enum { SB_BLOCK = 0, SB_BLOCK_T = 1, SB_ROW = 2 };
 enum { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
@@ -183,7 +184,7 @@ __device__ __forceinline__ int e8m0_of(float s, uint32_t& bad) {
 // choice because the compiler folds a run-time choice between an ordinary and a non-temporal store of the
 // same value into one ordinary store.
 template <class C, bool B_TRANS, int SBK, int GROUP, bool POW2, int EPI = EPI_STORE, bool STREAM = false>
-__global__ __launch_bounds__(C::NTHREADS, C::NW == 4 ? 2 : 1) void fg_gemm_kernel(GemmParams p) {
+__global__ __launch_bounds__(C::NTHREADS, 1) void fg_gemm_kernel(GemmParams p) {
     constexpr int BM = C::BM, BN = C::BN, NW = C::NW, MSUB = C::MSUB, NSUB = C::NSUB;
     constexpr int WAVE_M = C::WAVE_M, WAVE_N = C::WAVE_N;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(C::NTHREADS, C::NW == 4 ? 2 : 1) void fg_gemm_kerne
     // grouped) and the FP32-scale grouped Dgrad (1% faster); the other 128x128-block kernels F = 3; the
     // FP32-scale Wgrad spreads them over every row but the last (the loads must be out before the step's
     // hand-over barrier), the power-of-2 Wgrad F = 3 (5% faster than spreading).
-    constexpr int F = MSUB == 4 ? 2
+    constexpr int F = C::NW == 12 ? 2
                     : SBK == SB_ROW ? (POW2 ? 3 : MSUB - 1)
                     : (!POW2 && (!B_TRANS || GROUP == GRP_ROWS)) ? 4 : 3;
     static_assert(F <= MSUB - 1, "the next stage's loads are all issued before the last row's hand-over barrier");
@@ -1284,6 +1285,147 @@ __global__ __launch_bounds__(WideCfg::NTHREADS, 1) void fg_gemm_wide_kernel(Gemm
     }
 }
 
+// ---------------------------------------------------------------------------------------------------------
+// Fprop with epilogue on 128 x 128 x 128 workgroup tiles: 4 waves (2 x 2) of 64 x 64, for problems of few tiles.
+//
+// Such a problem gives a CU one tile or two, so nothing but its own loads ahead hides their latency: the large shapes'
+// two stages leave a K step waiting for a round trip to HBM (1.5 to 2.05 us a step of 256-row tiles). Here up to four
+// stages of 33 KB are in flight, filled as in fg_gemm_kernel (direct-to-LDS buffer loads, the same swizzle), and a wave
+// reads the next step's fragments while its MFMAs run on this one's, which 2 waves per SIMD leave the registers for.
+// The barrier of step kb says that every wave's part of stage kb + 1 has landed and that stage kb's fragments are read,
+// so its slot takes stage kb + STAGES. Every step issues the same loads (past the end the last block's again, into a
+// slot that nobody reads), so that one immediate count waits for the right stage throughout.
+// STAGES = 4: one workgroup a CU. STAGES = 2: two, which take turns at waiting. Measured (N = 7168): with a tile or
+// less a CU 48.1 against 57.7 us at M = 256, K = 7168, but 27.9 against 24.5 at N = 1024, K = 4096, where the fill
+// counts; with 336 tiles (M = 768) the single ones need a second round. M = 384, K = 7168: 48.9 us, 0.8 PFLOP/s; 88.5
+// with 256 x 192 tiles. Promotion is the VALU's in both scale modes: one FMA an element, with the scales as they are.
+template <int STAGES_>
+struct MidCfg {
+    static constexpr int NW = 4, NTHREADS = 256, BM = 128, BN = 128, WAVE = 64, SUB = 4, STAGES = STAGES_;
+    static constexpr int STAGE_A = BM * BK, STAGE_B = BN * BK;
+    static constexpr int SCALES = STAGE_A + STAGE_B, SCALE_B = SCALES + BM * 4;       // A scales, then 64 x the B scale
+    static constexpr int STAGE = SCALE_B + 256;
+    static constexpr int LDS_BYTES = STAGES * STAGE;
+    static constexpr int LOADS = 9;                                                  // a wave's per stage: 4 A, 4 B, 1 scales
+    static_assert(LDS_BYTES <= 160 * 1024 && NW * 32 * WAVE * 4 <= LDS_BYTES, "LDS");
+};
+
+// s_waitcnt with only the vector-memory count set.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+template <int STAGES>
+__global__ __launch_bounds__(MidCfg<STAGES>::NTHREADS, 4 / STAGES) void fg_gemm_mid_kernel(GemmParams p) {
+    using C = MidCfg<STAGES>;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int64_t M = p.M, N = p.N, K = p.K;
+    const int nkb = (int)(K / BK);
+    const int m_tiles = (int)((M + C::BM - 1) / C::BM), n_tiles = (int)((N + C::BN - 1) / C::BN);
+    // an XCD's tiles go down the rows first: they share the weight panel, the larger operand, in its L2
+    const int id = xcd_remap((int)blockIdx.x, m_tiles * n_tiles);
+    const int64_t m0 = (int64_t)(id % m_tiles) * C::BM, n0 = (int64_t)(id / m_tiles) * C::BN;
+
+    uint32_t a_off[4], b_off[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int row = (wave + 4 * u) * 8 + (lane >> 3);
+        const int64_t gm = m0 + row < M ? m0 + row : M - 1, gn = n0 + row < N ? n0 + row : N - 1;
+        const uint32_t chunk = ((lane & 7) ^ swz128(row)) << 4;
+        a_off[u] = (uint32_t)((gm - m0) * K) + chunk;
+        b_off[u] = (uint32_t)((gn - n0) * K) + chunk;
+    }
+    // waves 0 and 1 load the A scales of 64 rows each, waves 2 and 3 the block's scale (the same bytes)
+    const int64_t s_row = m0 + 64 * wave + lane < M ? m0 + 64 * wave + lane : M - 1;
+    const uint32_t s_off = wave < 2 ? (uint32_t)(s_row - m0) * 4 : 0;
+    const float* s_base = wave < 2 ? p.sa + m0 : p.sb + (n0 / 128) * nkb;
+    const int64_t s_step = wave < 2 ? p.sa_ld : 1;
+    auto issue = [&](int kb, int slot) {
+        const int k = kb < nkb ? kb : nkb - 1;
+        uint8_t* st = smem + slot * C::STAGE;
+        const auto ra = fg_buffer_rsrc(p.a + m0 * K + (int64_t)k * BK), rb = fg_buffer_rsrc(p.b + n0 * K + (int64_t)k * BK);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            fg_buffer_load_lds16(ra, st + (wave + 4 * u) * 1024, a_off[u]);
+            fg_buffer_load_lds16(rb, st + C::STAGE_A + (wave + 4 * u) * 1024, b_off[u]);
+        }
+        const auto rs = fg_buffer_rsrc(s_base + k * s_step);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, FG_LDS(st + (wave < 2 ? C::SCALES + wave * 256 : C::SCALE_B)), 4, s_off, 0, 0, 0);
+    };
+
+    const int lrow = lane & 15, g16 = lane >> 4;
+    const int frag_lo = lrow * BK + (((2 * g16) ^ swz128(lrow)) << 4);
+    const int frag_hi = lrow * BK + (((2 * g16 + 1) ^ swz128(lrow)) << 4);
+    v8i af[2][C::SUB], bf[2][C::SUB];
+    float sa[2][C::SUB], sb[2];
+    auto read = [&](int kb, int set) {
+        const uint8_t* st = smem + (kb & (STAGES - 1)) * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < C::SUB; i++) {
+            af[set][i] = frag_at(st + (wm * 64 + 16 * i) * BK, frag_lo, frag_hi);
+            bf[set][i] = frag_at(st + C::STAGE_A + (wn * 64 + 16 * i) * BK, frag_lo, frag_hi);
+            sa[set][i] = reinterpret_cast<const float*>(st + C::SCALES)[wm * 64 + 16 * i + lrow];
+        }
+        sb[set] = reinterpret_cast<const float*>(st + C::SCALE_B)[lane];
+    };
+    v4f acc[C::SUB][C::SUB];
+#pragma unroll
+    for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    if (nkb > 0) {
+#pragma unroll
+        for (int s = 0; s < C::STAGES; s++) issue(s, s);
+        wait_loads<(C::STAGES - 1) * C::LOADS>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        read(0, 0);
+    }
+    auto step = [&](int kb, auto set_tag) {
+        constexpr int set = decltype(set_tag)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<(C::STAGES - 2) * C::LOADS>();       // this wave's part of stage kb + 1
+        __builtin_amdgcn_s_waitcnt(0xC07F);             // its reads of stage kb (lgkmcnt 0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(kb + STAGES, kb & (STAGES - 1));
+        read(kb + 1, set ^ 1);
+        // the FMAs that fold tile t - LAG go behind the MFMA of tile t: a VALU read of a result waits for its MFMA
+        constexpr int LAG = 2, TILES = C::SUB * C::SUB;
+        v4f part[TILES];
+        float f[C::SUB];
+#pragma unroll
+        for (int i = 0; i < C::SUB; i++) f[i] = sa[set][i] * sb[set];
+#pragma unroll
+        for (int t = 0; t < TILES + LAG; t++) {
+            if (t < TILES)
+                part[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[set][t % C::SUB], af[set][t / C::SUB], v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, 127);
+            if (t >= LAG) {
+                const int i = (t - LAG) / C::SUB, j = (t - LAG) % C::SUB;
+#pragma unroll
+                for (int r = 0; r < 4; r++) acc[i][j][r] = __builtin_fmaf(part[t - LAG][r], f[i], acc[i][j][r]);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // four VALU operations
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // two LDS reads of the next step's fragments
+        }
+    };
+    int kb = 0;
+    for (; kb + 1 < nkb; kb += 2) {
+        step(kb, std::integral_constant<int, 0>{});
+        step(kb + 1, std::integral_constant<int, 1>{});
+    }
+    if (kb < nkb) step(kb, std::integral_constant<int, 0>{});
+
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();                                    // the stages are free
+    fg_store_epilogue<64>(p.ep, acc, smem + wave * (32 * 64 * 4), lane, m0 + wm * 64, M, n0 + wn * 64, N, p.out, p.out_bf16);
+}
+
 template <class C, bool B_TRANS, int SBK, int GROUP, bool POW2, int EPI = EPI_STORE, bool STREAM = false>
 hipError_t launch_one(const GemmParams& p, unsigned grid, hipStream_t stream) {
     auto kern = fg_gemm_kernel<C, B_TRANS, SBK, GROUP, POW2, EPI, STREAM>;
@@ -1377,35 +1519,68 @@ hipError_t launch_wide(const GemmParams& p, unsigned grid, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// The Fprop with its epilogue picks among the Fprop's shapes as fg_launch_gemm_fprop does, and takes 128 x 128 tiles
-// (two workgroups a CU) where they are estimated to end sooner: with few tiles a K step takes each shape the time its
-// loads need, and the smaller shape's come back sooner and leave fewer CUs without a tile. Time of a K step in us
-// with FP32 scales, from launches of less than one round (M = 16 to 768, N, K = 1024 to 18432, 80 problems).
-constexpr double kStep4 = 1.07, kStep4Full = 1.28, kStep12 = 1.55, kStep8 = 1.65, kStepWide = 1.85;
+// The Fprop with its epilogue picks among the Fprop's shapes as fg_launch_gemm_fprop does, and takes the 128 x 128 tiles
+// where they are estimated to end sooner. Time of a K step in us with FP32 scales, while the tiles fill less than
+// a round and more than half of one (M = 16 to 2048, N, K = 1024 to 18432, 66 problems; the 128 x 128 steps with
+// one and with two workgroups a CU).
+constexpr double kStepMid[2] = {0.74, 0.80}, kStepMid2[2] = {0.90, 1.20};
+constexpr double kStep12[2] = {1.50, 1.68}, kStep8[2] = {1.65, 1.86}, kStepWide[2] = {1.85, 2.05};
 
-int64_t rounds(int64_t tiles, int64_t per_round) { return (tiles + per_round - 1) / per_round; }
-
-double tile4_us(const GemmParams& p) {
-    const int64_t cus = fg_device_cus(), tiles = ((p.M + 127) / 128) * ((p.N + 127) / 128);
-    return (double)(p.K / BK) * (tiles <= cus ? kStep4 : kStep4Full * (double)rounds(tiles, 2 * cus));
+// K steps of all rounds of `tiles` tiles: [0] while a round is at most half full, [1] above (the CUs share the caches).
+double rounds_us(const GemmParams& p, int64_t tiles, int64_t per_round, const double (&step)[2]) {
+    const int64_t rounds = (tiles + per_round - 1) / per_round, rest = tiles - (rounds - 1) * per_round;
+    return (double)(p.K / BK) * ((double)(rounds - 1) * step[1] + (2 * rest > per_round ? step[1] : step[0]));
 }
-double large_tile_us(const GemmParams& p) {
+int64_t mid_tiles(const GemmParams& p) { return ((p.M + 127) / 128) * ((p.N + 127) / 128); }
+bool mid_single(const GemmParams& p) { return mid_tiles(p) <= fg_device_cus() && p.K / BK >= 40; }
+
+double mid_tile_us(const GemmParams& p) {
+    return mid_single(p) ? rounds_us(p, mid_tiles(p), fg_device_cus(), kStepMid) : rounds_us(p, mid_tiles(p), 2 * fg_device_cus(), kStepMid2);
+}
+// The shape that is estimated to end first, and its time. Unlike the Fprop's rules this weighs 256 x 288 against
+// 256 x 192 directly (M = 1024, N = 18432, K = 7168: 122 against 188 us). A forced shape goes by the Fprop's rules.
+enum EpilogueShape { SHAPE_MID, SHAPE_12, SHAPE_8, SHAPE_WIDE };
+EpilogueShape epilogue_shape(const GemmParams& p, double& us) {
+    us = 0.0;
+    if (const char* force = getenv("FG_GEMM_TILE")) {
+        if (strcmp(force, "128x128") == 0) return SHAPE_MID;
+        return use_wide(p) ? SHAPE_WIDE : use_cfg8(p, GRP_NONE) ? SHAPE_8 : SHAPE_12;
+    }
     const int64_t cus = fg_device_cus(), m_tiles = (p.M + 255) / 256;
-    const bool wide = use_wide(p), cfg8 = use_cfg8(p, GRP_NONE);
-    const int64_t bn = wide ? WideCfg::BN : cfg8 ? Cfg8::BN : Cfg12::BN;
-    return (double)(p.K / BK) * (wide ? kStepWide : cfg8 ? kStep8 : kStep12) * (double)rounds(m_tiles * ((p.N + bn - 1) / bn), cus);
+    EpilogueShape best = SHAPE_MID;
+    us = mid_tile_us(p);
+    auto consider = [&](EpilogueShape shape, int64_t bn, const double (&step)[2]) {
+        const double t = rounds_us(p, m_tiles * ((p.N + bn - 1) / bn), cus, step);
+        if (t < us) us = t, best = shape;
+    };
+    consider(SHAPE_12, Cfg12::BN, kStep12);
+    consider(SHAPE_8, Cfg8::BN, kStep8);
+    if ((int64_t)WideCfg::BN * p.K < (1ll << 32)) consider(SHAPE_WIDE, WideCfg::BN, kStepWide);   // as in use_wide
+    return best;
+}
+
+template <int STAGES>
+hipError_t launch_mid(const GemmParams& p, hipStream_t stream) {
+    using C = MidCfg<STAGES>;
+    auto kern = fg_gemm_mid_kernel<STAGES>;
+    static std::atomic<uint64_t> lds_limit_set{0};
+    const hipError_t e = fg_set_lds_limit_once((const void*)kern, C::LDS_BYTES, lds_limit_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)mid_tiles(p)), dim3(C::NTHREADS), C::LDS_BYTES, stream, p);
+    return hipGetLastError();
 }
 
 template <bool POW2>
 hipError_t launch_epilogue(const GemmParams& p, hipStream_t stream) {
-    if (!getenv("FG_GEMM_TILE") && tile4_us(p) < large_tile_us(p))
-        return launch_one<Cfg4, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg4>(p, GRP_NONE), stream);
-    if (use_wide(p)) {
-        const unsigned grid = (unsigned)(((p.M + WideCfg::BM - 1) / WideCfg::BM) * ((p.N + WideCfg::BN - 1) / WideCfg::BN));
-        return launch_wide<POW2, false, EPI_ACT>(p, grid, stream);
+    double us;
+    switch (epilogue_shape(p, us)) {
+        case SHAPE_MID: return mid_single(p) ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
+        case SHAPE_12: return launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg12>(p, GRP_NONE), stream);
+        case SHAPE_8: return launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg8>(p, GRP_NONE), stream);
+        default: break;
     }
-    if (use_cfg8(p, GRP_NONE)) return launch_one<Cfg8, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg8>(p, GRP_NONE), stream);
-    return launch_one<Cfg12, false, SB_BLOCK, GRP_NONE, POW2, EPI_ACT>(p, grid_for<Cfg12>(p, GRP_NONE), stream);
+    const unsigned grid = (unsigned)(((p.M + WideCfg::BM - 1) / WideCfg::BM) * ((p.N + WideCfg::BN - 1) / WideCfg::BN));
+    return launch_wide<POW2, false, EPI_ACT>(p, grid, stream);
 }
 
 }  // namespace
@@ -1429,8 +1604,9 @@ double fg_gemm_epilogue_us(int64_t M, int64_t N, int64_t K) {
     if (getenv("FG_GEMM_TILE")) return 0.0;      // a forced tile: these kernels
     GemmParams p{};
     p.M = M; p.N = N; p.K = K;
-    const double small = tile4_us(p), large = large_tile_us(p);
-    return 4.0 + (small < large ? small : large);
+    double us;
+    epilogue_shape(p, us);
+    return 6.0 + us;
 }
 
 hipError_t fg_launch_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,

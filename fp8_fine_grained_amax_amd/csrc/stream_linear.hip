@@ -121,11 +121,11 @@ constexpr int64_t kWideLinear = 4096;  // output columns from which workgroups t
 }  // namespace
 
 // Estimated time in us of the weight-streaming Linear: 4 us of launch and latency, then a pass over the weights for
-// every 64 rows, the first from HBM and the others from the caches at about the same 5.2 TB/s (3.2 where N leaves 16-row
+// every 64 rows, the first from HBM and the others from the caches at about the same 5.2 TB/s (3.0 where N leaves 16-row
 // workgroups only), and an LDS exchange that the tokens' operands add to the first pass. Measured: N = 18432,
 // K = 7168: 31 us at M = 16, 48 at 64, 66 at 128, 115 at 256; N = K = 7168: 13.5, 19.5, 29.5, 48.5.
 double fg_stream_linear_us(int64_t M, int64_t N, int64_t K) {
-    const double pass = (double)N * (double)K / (N >= kWideLinear ? 5.2e6 : 3.2e6);
+    const double pass = (double)N * (double)K / (N >= kWideLinear ? 5.2e6 : 3.0e6);
     return 4.0 + pass * (M <= 16 ? 1.0 : M <= 32 ? 1.2 : (double)((M + 63) / 64) + 0.6);
 }
 

@@ -80,7 +80,7 @@ def test_linear_epilogues(M, N, kind, types):
 
 @pytest.mark.parametrize("M,N,types", [(300, 576, "fff"), (300, 580, "bbf"), (257, 333, "bfb"), (64, 1160, "ffb")])
 @pytest.mark.parametrize("kind", ["gelu", "relu"])
-@pytest.mark.parametrize("tile", ["256x192", "256x256", "256x288"])
+@pytest.mark.parametrize("tile", ["128x128", "256x192", "256x256", "256x288"])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_linear_epilogue_on_every_tile(M, N, types, kind, tile, pow2, monkeypatch):
     monkeypatch.setenv("FG_GEMM_TILE", tile)
@@ -92,15 +92,32 @@ def test_linear_epilogue_on_every_tile(M, N, types, kind, tile, pow2, monkeypatc
     check_linear(ops, y, kind, bias, residual)
 
 
-@pytest.mark.parametrize("M,N,K", [(640, 4096, 1024), (1000, 3000, 512), (2048, 2056, 256)])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (128, 128, 256), (129, 257, 384), (640, 4096, 1024), (1000, 3001, 512),
+                                   (300, 200, 640), (130, 130, 768), (5, 2056, 1152), (256, 128, 4736), (2048, 2056, 256), (1000, 3000, 512),
+                                   (1, 1, 5120), (300, 200, 5248), (64, 130, 5376), (129, 264, 5504)])
 @pytest.mark.parametrize("pow2", [False, True])
-def test_linear_on_small_tiles(M, N, K, pow2):
-    """Sizes whose launches take the 128x128 tiles."""
+def test_linear_on_small_tiles(M, N, K, pow2, monkeypatch):
+    """The 128x128 tiles with two stages and, from 40 blocks of 128 on, with four."""
+    monkeypatch.setenv("FG_GEMM_TILE", "128x128")
     ops = linear_case(M, M, N, K, pow2)
     bias, residual = rand(1, N), rand(2, M, N)
     y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=device())
     fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_SILU, residual=residual, y=y, pow2=pow2)
     check_linear(ops, y, "silu", bias, residual)
+
+
+@pytest.mark.parametrize("M,K", [(16, 640), (200, 1152), (16, 5120), (200, 5248)])
+def test_linear_small_tiles_exact(M, K, monkeypatch):
+    """Small whole numbers: the sum is exact, so each output names the stages it was made of."""
+    monkeypatch.setenv("FG_GEMM_TILE", "128x128")
+    g = torch.Generator().manual_seed(M)
+    x, w = torch.randint(-4, 5, (M, K), generator=g).float(), torch.randint(-2, 3, (272, K), generator=g).float()
+    sx = torch.exp2(torch.randint(-1, 2, (K // 128, M), generator=g).float())
+    sw = torch.exp2(torch.randint(-1, 2, (3, K // 128), generator=g).float())
+    want = (x * sx.t().repeat_interleave(128, 1)) @ (w * sw.repeat_interleave(128, 0)[:272].repeat_interleave(128, 1)).t()
+    y = fg.fg_fp8_gemm_fprop_epilogue(x.to(torch.float8_e4m3fn).view(torch.uint8).to(device()), sx.to(device()),
+                                      w.to(torch.float8_e4m3fn).view(torch.uint8).to(device()), sw.to(device()), out_dtype=torch.float32)
+    assert torch.equal(y.cpu(), want)
 
 
 @pytest.mark.parametrize("M", [1, 16, 64, 65, 256])
