@@ -7,6 +7,7 @@
 namespace {
 
 constexpr int64_t kMaxGrid = 2147483647LL;
+constexpr int64_t kMaxThreads = (1LL << 32) - 1; // of a launch along one dimension
 constexpr int64_t kMaxContraction = 1LL << 24;   // as in the other GEMMs: 32-bit operand offsets
 constexpr int64_t kMaxCols = 1LL << 23;          // 32-bit offsets inside a 128-row block of up to 2 F codes or F fp32 values
 constexpr int64_t kMaxRows = 1LL << 25;          // and inside a 128-column block of a tiling along the rows
@@ -14,6 +15,7 @@ constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxExpertDim = 1LL << 20;
 constexpr int64_t kMaxTokens = 64;
 constexpr int64_t kMaxStreamRows = 4096;         // a grid of 64 blocks of rows; its estimate lies far above the tiles' by then
+constexpr int64_t kMaxStreamCols = 1LL << 26;    // kMaxThreads: 512 threads to 16 columns
 constexpr int kMaxTopk = 32, kMaxExperts = 2048;
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -50,7 +52,7 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
     const FgEpilogue e{bias, residual, ld_res, bias && bias_type == FG_OUT_BF16,
                        residual && residual_type == FG_OUT_BF16, (int)act, vector_ok};
     const int bf16 = out == FG_OUT_BF16;
-    if (M <= kMaxStreamRows && fg_stream_linear_us(M, N, K) <= fg_gemm_epilogue_us(M, N, K))
+    if (M <= kMaxStreamRows && N <= kMaxStreamCols && fg_stream_linear_us(M, N, K) <= fg_gemm_epilogue_us(M, N, K))
         return fg_status_from_hip(fg_launch_stream_linear(xq, sx, wq, sw, M, N, K, e, y, bf16, stream));
     return fg_status_from_hip(
         fg_launch_gemm_fprop_epilogue(xq, sx, wq, sw, M, N, K, e, y, bf16, scales == FG_SCALE_POW2, stream));
@@ -63,7 +65,7 @@ fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t 
     if (ld_z < (gated ? 2 : 1) * F) return FG_ERR_INVALID_ARG;
     if (rows == 0 || F == 0) return FG_OK;
     if (!z || !zq || !sz || !aq || !sa) return FG_ERR_INVALID_ARG;
-    if (F % 128 != 0 || prod_over(F / 128, cdiv(rows, 16), kMaxGrid)) return FG_ERR_UNSUPPORTED_SHAPE;
+    if (F % 128 != 0 || prod_over(F / 128, cdiv(rows, 32), kMaxThreads / 256)) return FG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(z, 16) || ld_z % 8 != 0 || !aligned(zq, 16) || !aligned(aq, 16) || !aligned(sz, 4) || !aligned(sa, 4))
         return FG_ERR_MISALIGNED;
     return fg_status_from_hip(fg_launch_act_fwd((const uint16_t*)z, rows, F, ld_z, (int)act, gated, mode == FG_SCALE_POW2,
@@ -86,7 +88,7 @@ fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* 
     if (F == 0 || (rows == 0 && !dbias)) return FG_OK;
     if (!dzq_rows != !sdz_rows || !aq_rows != !sa_rows) return FG_ERR_INVALID_ARG;
     if (rows > 0 && (!zq || !sz || !da || !dzq_cols || !sdz_cols)) return FG_ERR_INVALID_ARG;
-    if (F % 128 != 0 || ((dzq_rows || aq_rows) && rows % 128 != 0) || prod_over(F / 128, cdiv(rows, 128), kMaxGrid))
+    if (F % 128 != 0 || ((dzq_rows || aq_rows) && rows % 128 != 0) || prod_over(F / 128, cdiv(rows, 128), kMaxThreads / 512))
         return FG_ERR_UNSUPPORTED_SHAPE;
     const int64_t need = dbias ? fg_act_checkpoint_bwd_workspace(rows, F, gated) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return FG_ERR_INVALID_ARG;
@@ -119,6 +121,8 @@ fg_status fg_moe_few_tokens(const void* x, int64_t ld_x, const int32_t* ids, con
     if (T > kMaxTokens || topk > kMaxTopk || E > kMaxExperts || H > kMaxExpertDim || I > kMaxExpertDim || H % 128 != 0 ||
         I % 128 != 0 || ld_x > kMaxStride || ld_y > kMaxStride)
         return FG_ERR_UNSUPPORTED_SHAPE;
+    // the up-projection: 256 threads to 32 hidden columns of an expert
+    if (prod_over(T * topk < E ? T * topk : E, I / 32, kMaxThreads / 256)) return FG_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || H == 0) return FG_OK;
     if (!x || !ids || !weights || !y || (I > 0 && (!w1q || !s1 || !w2q || !s2))) return FG_ERR_INVALID_ARG;
     const int64_t need = fg_moe_few_tokens_workspace(T, topk, H, I);

@@ -22,7 +22,7 @@ __device__ __forceinline__ float fg_gelu_sigmoid(float z, float& z2) {
 
 template <int ACT>
 __device__ __forceinline__ float fg_act_value(float z) {
-    if constexpr (ACT == FG_ACT_RELU) return __builtin_fmaxf(z, 0.0f);
+    if constexpr (ACT == FG_ACT_RELU) return __builtin_elementwise_maximum(z, 0.0f);      // a NaN stays one
     if constexpr (ACT == FG_ACT_SILU) return z * fg_sigmoid(z);
     if constexpr (ACT == FG_ACT_GELU_TANH) {
         // without the clamp: where z^2 overflows, the sigmoid's argument is infinite and it 0 or 1 all the same.
@@ -38,8 +38,8 @@ __device__ __forceinline__ float fg_act_value(float z) {
 template <int ACT>
 __device__ __forceinline__ void fg_act_both(float z, float& a, float& slope) {
     if constexpr (ACT == FG_ACT_RELU) {
-        a = __builtin_fmaxf(z, 0.0f);
-        slope = z > 0.0f ? 1.0f : 0.0f;
+        a = fg_act_value<FG_ACT_RELU>(z);
+        slope = z <= 0.0f ? 0.0f : 1.0f;
     } else if constexpr (ACT == FG_ACT_SILU) {
         const float k = fg_sigmoid(z);
         a = z * k;
@@ -66,15 +66,16 @@ __device__ __forceinline__ float fg_act_any(int act, float z) {
 
 // Scales of N groups of fp32 values from their max-abs: as fg_scale_from_amax_bits, whose corrected product equals
 // the correctly rounded amax / 448 while its remainder is exact; below 2^-80 (rare: one branch for all the groups) the
-// division itself. Call with the whole wave active.
+// division itself. A max-abs that overflowed counts as the largest finite one: the codes of the infinite values are
+// then NaN (inf - inf in fg_quot_arg), and the scale stays a number. Call with the whole wave active.
 template <int N>
 __device__ __forceinline__ void fg_scales_from_amax(const float (&amax)[N], int pow2, float (&s)[N]) {
     const float c = 0x1.24924ap-9f;                     // RN(1/448)
     float least = amax[0];
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const float q0 = amax[i] * c;
-        s[i] = __builtin_fmaf(__builtin_fmaf(-q0, 448.0f, amax[i]), c, q0);
+        const float m = __builtin_fminf(amax[i], 0x1.fffffep127f), q0 = m * c;
+        s[i] = __builtin_fmaf(__builtin_fmaf(-q0, 448.0f, m), c, q0);
         least = __builtin_fminf(least, amax[i]);
     }
     if (__builtin_amdgcn_ballot_w64(least < 0x1p-80f) != 0) {

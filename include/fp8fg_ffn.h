@@ -8,7 +8,8 @@
  * checked on the host before any HIP call, and a failed check enqueues nothing. Formats, the quantization
  * rule and the GEMM rule are those of fp8fg.h; where a quantizer below takes values that the kernel itself
  * computed, the rule is applied to their fp32 values, which are not rounded to bf16 first. Inputs must be
- * finite unless stated otherwise.
+ * finite unless stated otherwise; of values that overflow fp32 on the way (a gate times its factor), an infinite one gets
+ * the code NaN, and its tile's scale comes from the largest finite float.
  */
 #ifndef FP8FG_FFN_H
 #define FP8FG_FFN_H
@@ -47,7 +48,7 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
  *       factor: a = act(gate) * up).
  *   zq  u8 [rows][W], sz f32 [W/128][rows]: fg_quantize_act_1x128(z, FG_ALONG_COLS, mode), bit for bit.
  *   aq  u8 [rows][F], sa f32 [F/128][rows]: a in the same tiling, the next Linear's input.
- *   F % 128 == 0, F <= 2^23, rows <= 2^25. z, zq, aq 16-byte aligned; ld_z % 8 == 0; sz, sa 4-byte aligned.
+ *   F % 128 == 0, F <= 2^23, rows <= 2^25, F * ceil(rows / 32) < 2^31. z, zq, aq 16-byte aligned; ld_z % 8 == 0; sz, sa 4-byte aligned.
  *   rows == 0 or F == 0 is a no-op. */
 fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t ld_z, fg_act act, int gated,
                                 fg_scale_mode mode, uint8_t* zq, float* sz, uint8_t* aq, float* sa, hipStream_t stream);
@@ -67,8 +68,7 @@ fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t 
  *            where that is 0 or dbias is NULL. 4-byte aligned. One call's contents mean nothing to the next; calls
  *            that may run at the same time need workspaces of their own.
  *   F % 128 == 0; rows % 128 == 0 where a tiling along the rows is asked for, any rows otherwise; F and ld_da at most
- *   2^23, rows at most 2^25. zq, da, dzq_cols,
- *   dzq_rows, aq_rows 16-byte aligned, ld_da a multiple of 16 bytes; the fp32 outputs and sz 4-byte aligned.
+ *   2^23, rows at most 2^25, F * ceil(rows / 128) < 2^30. zq, da, dzq_cols, dzq_rows, aq_rows 16-byte aligned, ld_da a multiple of 16 bytes; the fp32 outputs and sz 4-byte aligned.
  *   rows == 0 or F == 0: no-op, but for dbias, which becomes 0. */
 int64_t fg_act_checkpoint_bwd_workspace(int64_t rows, int64_t F, int gated);
 fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* da, fg_out_dtype da_type, int64_t ld_da,
@@ -90,7 +90,8 @@ fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* 
  *   workspace   fg_moe_few_tokens_workspace(T, topk, H, I) bytes, 16-byte aligned; calls that may run at the same
  *               time need workspaces of their own.
  *   y    [T][H] f32 or bf16, row stride ld_y.
- *   0 <= T <= 64, 1 <= topk <= 32, 1 <= E <= 2048, H % 128 == 0, I % 128 == 0, H and I at most 2^20. x, w1q, w2q, y
+ *   0 <= T <= 64, 1 <= topk <= 32, 1 <= E <= 2048, H % 128 == 0, I % 128 == 0, H and I at most 2^20, I * min(E, T * topk) <
+ *   2^29. x, w1q, w2q, y
  *   16-byte aligned, ld_x % 8 == 0; ids, weights, s1, s2 4-byte aligned; ld_y >= H. T == 0 or H == 0 is a no-op;
  *   I == 0 writes zeros. x, the weights and the workspace must not overlap y. */
 int64_t fg_moe_few_tokens_workspace(int64_t T, int32_t topk, int64_t H, int64_t I);

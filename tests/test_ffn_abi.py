@@ -104,6 +104,19 @@ def test_workspace_sizes(L):
         assert m(*a) < m(*b), (a, b)
 
 
+def test_launches_past_32_bits_of_threads_are_refused(L):
+    def fwd(rows, F):
+        return L.fg_act_checkpoint_fwd(A, rows, F, 2 * F, 3, 1, 0, B, B, B, B, None)
+    def bwd(rows, F):
+        return L.fg_act_checkpoint_bwd(A, A, A, 0, F, rows, F, 3, 1, 0, B, B, None, None, None, None, None, None, 0, None)
+    def moe(T, topk, E, I):
+        return L.fg_moe_few_tokens(A, 256, A, A, T, topk, A, A, A, A, E, 256, I, 3, 0, None, 0, B, 256, 1, None)
+    assert fwd(1 << 25, 2048) == SHAPE and fwd(1 << 25, 1 << 23) == SHAPE
+    assert bwd(1 << 25, 4096) == SHAPE and bwd((1 << 25) - 5, 4096) == SHAPE
+    assert moe(64, 32, 2048, 1 << 18) == SHAPE and moe(16, 32, 512, 1 << 20) == SHAPE
+    assert moe(64, 32, 2048, (1 << 18) - 128) == INVALID and moe(64, 32, 256, 1 << 20) == INVALID    # no workspace: within limits
+
+
 def test_binding_refuses_cpu_tensors():
     z = torch.zeros(4, 256, dtype=torch.bfloat16)
     u = torch.zeros(4, 256, dtype=torch.uint8)

@@ -329,6 +329,41 @@ def test_act_gradient_against_differences():
         ref.check_tiles(r.dzq_cols, r.sdz_cols, dz, err + 1e-9 * (1 + da.double().abs().repeat(1, 2)) * (1 + z.abs()), False, kind)
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+def test_act_overflow_stays_visible(pow2):
+    """A product that overflows becomes a NaN code under a finite scale; the other tiles are what they are without it."""
+    z = rand(1, 128, 512)
+    z[3, 10], z[3, 266] = 3e38, 3e38
+    zq, sz, aq, sa = fg.fg_act_checkpoint_fwd(z, fg.FG_ACT_SILU, gated=True, pow2=pow2)
+    assert bool(torch.isfinite(sa).all()) and bool(torch.isfinite(sz).all()) and not bool(((zq & 0x7F) == 0x7F).any())
+    assert ((aq & 0x7F) == 0x7F).nonzero().tolist() == [[3, 10]]
+    z = rand(2, 128, 512) + 4
+    z[5, 140] = z[5, 396] = 4
+    zq, sz = fg.fg_quantize_act_1x128(z)
+    da = torch.ones(128, 256, device=device())
+    calm = fg.fg_act_checkpoint_bwd(zq, sz, da, fg.FG_ACT_SILU, gated=True, pow2=pow2)
+    da[5, 140] = 3.4e38
+    r = fg.fg_act_checkpoint_bwd(zq, sz, da, fg.FG_ACT_SILU, gated=True, pow2=pow2, bias_grad=True)
+    for s in (r.sdz_cols, r.sdz_rows, r.sa_rows):
+        assert bool(torch.isfinite(s).all()) and bool((s > 0).all())
+    assert ((r.dzq_cols & 0x7F) == 0x7F).nonzero().tolist() == [[5, 140], [5, 396]]
+    assert ((r.dzq_rows & 0x7F) == 0x7F).nonzero().tolist() == [[140, 5], [396, 5]]
+    keep = torch.ones(128, dtype=torch.bool)
+    keep[5] = False
+    assert torch.equal(r.dzq_cols[keep.to(device())], calm.dzq_cols[keep.to(device())]) and torch.equal(r.aq_rows, calm.aq_rows)
+    assert (~torch.isfinite(r.dbias)).nonzero().flatten().tolist() == [140, 396]
+
+
+@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("kind", ["none", "relu", "gelu", "silu"])
+def test_linear_nan_stays_visible(M, kind):
+    ops = linear_case(M, M, 136, 256, False)
+    bias = rand(1, 136)
+    bias[7] = float("nan")
+    y = fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=act_code(kind))
+    assert bool(torch.isnan(y[:, 7]).all()) and int(torch.isnan(y).sum()) == M
+
+
 def test_act_empty():
     dev = device()
     z = torch.empty((0, 256), dtype=torch.bfloat16, device=dev)
