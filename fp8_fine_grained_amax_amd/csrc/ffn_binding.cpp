@@ -146,6 +146,15 @@ void check(fg_status s, const char* what) {
     fail("%s: %s", what, fg_status_string(s));
 }
 
+// A library call with the interpreter's lock released: a launch waits where the queue is full.
+template <class Call>
+void run(const char* what, Call&& call) {
+    PyThreadState* state = PyEval_SaveThread();
+    const fg_status s = call();
+    PyEval_RestoreThread(state);
+    check(s, what);
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 PyObject* tuple(const std::vector<at::Tensor>& v) {
@@ -196,10 +205,13 @@ PyObject* linear(PyObject* const* a) {
     }
     const c10::DeviceGuard guard(d);
     const at::Tensor y = output(a[8], "y", type, {M, N}, d);
-    check(fg_fp8_gemm_fprop_epilogue(x, (const float*)sx.data_ptr(), w, (const float*)sw.data_ptr(), M, N, K, bias,
-                                     (fg_out_dtype)bias_type, act, residual, (fg_out_dtype)res_type, ld_res, y.data_ptr(),
-                                     type == at::kBFloat16 ? FG_OUT_BF16 : FG_OUT_F32, mode(a[9]), stream(d)),
-          "fg_fp8_gemm_fprop_epilogue");
+    const fg_scale_mode scales = mode(a[9]);
+    const hipStream_t on = stream(d);
+    run("fg_fp8_gemm_fprop_epilogue", [&] {
+        return fg_fp8_gemm_fprop_epilogue(x, (const float*)sx.data_ptr(), w, (const float*)sw.data_ptr(), M, N, K, bias,
+                                          (fg_out_dtype)bias_type, act, residual, (fg_out_dtype)res_type, ld_res, y.data_ptr(),
+                                          type == at::kBFloat16 ? FG_OUT_BF16 : FG_OUT_F32, scales, on);
+    });
     return THPVariable_Wrap(y);
 }
 
@@ -218,9 +230,12 @@ PyObject* act_forward(PyObject* const* a) {
     const at::Tensor sz = output(a[5], "sz", at::kFloat, {cdiv(W, 128), rows}, d);
     const at::Tensor aq = output(a[6], "aq", at::kByte, {rows, F}, d);
     const at::Tensor sa = output(a[7], "sa", at::kFloat, {cdiv(F, 128), rows}, d);
-    check(fg_act_checkpoint_fwd(z.data_ptr(), rows, F, ld, act, gated, mode(a[3]), (uint8_t*)zq.data_ptr(), (float*)sz.data_ptr(),
-                                (uint8_t*)aq.data_ptr(), (float*)sa.data_ptr(), stream(d)),
-          "fg_act_checkpoint_fwd");
+    const fg_scale_mode scales = mode(a[3]);
+    const hipStream_t on = stream(d);
+    run("fg_act_checkpoint_fwd", [&] {
+        return fg_act_checkpoint_fwd(z.data_ptr(), rows, F, ld, act, gated, scales, (uint8_t*)zq.data_ptr(), (float*)sz.data_ptr(),
+                                     (uint8_t*)aq.data_ptr(), (float*)sa.data_ptr(), on);
+    });
     return tuple({zq, sz, aq, sa});
 }
 
@@ -263,10 +278,13 @@ PyObject* act_backward(PyObject* const* a) {
     }
     if (need || !is_none(a[10])) ws = workspace(a[10], need, d);
     auto at_ = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-    check(fg_act_checkpoint_bwd((const uint8_t*)zq.data_ptr(), sz, da.data_ptr(), (fg_out_dtype)da_type, ld, rows, F, act, gated,
-                                mode(a[5]), (uint8_t*)qc.data_ptr(), (float*)sc.data_ptr(), (uint8_t*)at_(qr), (float*)at_(sr),
-                                (uint8_t*)at_(ar), (float*)at_(sa), (float*)at_(db), at_(ws), ws.defined() ? ws.numel() : 0, stream(d)),
-          "fg_act_checkpoint_bwd");
+    const fg_scale_mode scales = mode(a[5]);
+    const hipStream_t on = stream(d);
+    run("fg_act_checkpoint_bwd", [&] {
+        return fg_act_checkpoint_bwd((const uint8_t*)zq.data_ptr(), sz, da.data_ptr(), (fg_out_dtype)da_type, ld, rows, F, act, gated,
+                                     scales, (uint8_t*)qc.data_ptr(), (float*)sc.data_ptr(), (uint8_t*)at_(qr), (float*)at_(sr),
+                                     (uint8_t*)at_(ar), (float*)at_(sa), (float*)at_(db), at_(ws), ws.defined() ? ws.numel() : 0, on);
+    });
     return tuple({qc, sc, qr, sr, ar, sa, db});
 }
 
@@ -294,10 +312,13 @@ PyObject* moe(PyObject* const* a) {
     const int out = real_type(y, "y");
     const int64_t ld_y = matrix(y, "y", T, H, d);
     const at::Tensor ws = workspace(a[11], fg_moe_few_tokens_workspace(T, (int32_t)topk, H, I), d);
-    check(fg_moe_few_tokens(x.data_ptr(), ld_x, id, weights, T, (int32_t)topk, w1q, (const float*)s1.data_ptr(), w2q,
-                            (const float*)s2.data_ptr(), (int32_t)E, H, I, act, mode(a[10]), ws.data_ptr(), ws.numel(), y.data_ptr(),
-                            ld_y, (fg_out_dtype)out, stream(d)),
-          "fg_moe_few_tokens");
+    const fg_scale_mode scales = mode(a[10]);
+    const hipStream_t on = stream(d);
+    run("fg_moe_few_tokens", [&] {
+        return fg_moe_few_tokens(x.data_ptr(), ld_x, id, weights, T, (int32_t)topk, w1q, (const float*)s1.data_ptr(), w2q,
+                                 (const float*)s2.data_ptr(), (int32_t)E, H, I, act, scales, ws.data_ptr(), ws.numel(), y.data_ptr(),
+                                 ld_y, (fg_out_dtype)out, on);
+    });
     return THPVariable_Wrap(y);
 }
 
