@@ -541,6 +541,19 @@ def test_moe_most_choices():
     check_moe(y, (x, ids % 8, weights, q1, s1, q2, s2), "silu", False)
 
 
+@pytest.mark.parametrize("T,topk", [(1, 32), (2, 32), (3, 32), (16, 4), (16, 32), (13, 5), (17, 32)])
+def test_moe_choices_again_and_out_of_range(T, topk):
+    """Up to 32 choices a token that repeat and miss the experts, on both sides of 64 choices and of 16 tokens."""
+    E, H, I = 12, 256, 128
+    w = experts(1, E, H, I)
+    g = torch.Generator().manual_seed(T * topk)
+    ids = torch.randint(-2, E + 2, (T, topk), generator=g, dtype=torch.int32).to(device())
+    weights = (torch.rand(T, topk, generator=g) / topk).to(device())
+    x = rand(2, T, H)
+    y = fg.fg_moe_few_tokens(x, ids, weights, *w, out_dtype=torch.float32)
+    check_moe(y, (x, ids, weights, *w), "silu", False)
+
+
 # ---- together -------------------------------------------------------------------------------------------
 
 def mlp_step(x, dy, w1, b1, w2, b2, gated, kind):
