@@ -116,29 +116,60 @@ hipError_t launch_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, 
     return hipGetLastError();
 }
 
-constexpr int64_t kWideLinear = 4096;  // output columns from which workgroups take 32 of them
+// Which workgroup a problem gets: columns x rows, waves that split the contraction. A wider tile moves fewer bytes through
+// L2 (an operand byte serves more products), a smaller one leaves more workgroups and waves to hide a load's latency
+// with; so the widest that still fills the CUs. Boundaries and estimates from 15 weights (N, K = 1024 to 18432) at 17 to
+// 1024 rows; in us, N x K at M rows:
+//   up to 16 rows   32 columns from N = 4096 on (7168 x 18432, 16: 28.4 against 35.7), 16 below
+//   up to 32 rows   32x32, 16x32 below N = 4096 (7168 x 7168, 32: 14.1 against 21; 2048 x 16384, 32: 22.6 against 18.2)
+//   more, by the number of 32x32 tiles:
+//     below 384     32x32 (2048 x 16384, 128: 21.1; 28.8 with 32x64)
+//     below 800     32x64 (1024 x 4096, 512: 9.7; 10.5 with 32x32, 11.7 with 64x32)
+//     above         64x32 (2001 x 2048, 512: 11.6; 14.5 with 32x64), and
+//                   64x64 where one round of two a CU holds them all and fills it (7168 x 18432, 200: 75; 98 with 64x32)
+enum LinearShape { L16x16, L32x16, L16x32, L32x32, L32x64, L64x32, L64x64 };
+
+int64_t linear_tiles(int64_t M, int64_t N, int cols, int rows) { return ((N + cols - 1) / cols) * ((M + rows - 1) / rows); }
+
+LinearShape linear_shape(int64_t M, int64_t N) {
+    const bool wide = N >= 4096;
+    if (M <= 16) return wide ? L32x16 : L16x16;
+    if (M <= 32) return wide ? L32x32 : L16x32;
+    const int64_t small = linear_tiles(M, N, 32, 32), large = linear_tiles(M, N, 64, 64);
+    if (small < 384) return L32x32;
+    if (small < 800) return L32x64;
+    return large >= 384 && large <= 512 ? L64x64 : L64x32;
+}
 
 }  // namespace
 
-// Estimated time in us of the weight-streaming Linear: 4 us of launch and latency, then a pass over the weights for
-// every 64 rows, the first from HBM and the others from the caches at about the same 5.2 TB/s (3.0 where N leaves 16-row
-// workgroups only), and an LDS exchange that the tokens' operands add to the first pass. Measured: N = 18432,
-// K = 7168: 31 us at M = 16, 48 at 64, 66 at 128, 115 at 256; N = K = 7168: 13.5, 19.5, 29.5, 48.5.
+// Estimated time in us of the weight-streaming Linear: launch and latency, then the larger of its tiles' K steps and the
+// weights' bytes from HBM (slower the more rows share the waits).
 double fg_stream_linear_us(int64_t M, int64_t N, int64_t K) {
-    const double pass = (double)N * (double)K / (N >= kWideLinear ? 5.2e6 : 3.0e6);
-    return 4.0 + pass * (M <= 16 ? 1.0 : M <= 32 ? 1.2 : (double)((M + 63) / 64) + 0.6);
+    const double steps = (double)(K / BK), bytes = (double)N * (double)K;
+    auto larger = [](double a, double b) { return a > b ? a : b; };
+    switch (linear_shape(M, N)) {
+        case L32x16: return 4.0 + bytes / 5.2e6;
+        case L16x16:
+        case L16x32: return 4.0 + bytes / 3.0e6;
+        case L32x32: return 3.5 + larger(0.6e-3 * steps * (double)linear_tiles(M, N, 32, 32), bytes / 3.7e6);
+        case L32x64: return 3.5 + 1.0e-3 * steps * (double)linear_tiles(M, N, 32, 64) + bytes / 17e6;
+        case L64x32: return 3.5 + larger(0.83e-3 * steps * (double)linear_tiles(M, N, 64, 32), bytes / 2.5e6);
+        case L64x64: return 5.0 + larger(0.52 * steps, bytes / 3.0e6);
+    }
+    return 0.0;
 }
 
 hipError_t fg_launch_stream_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                    int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, hipStream_t stream) {
-    // 32 output columns a workgroup share each token tile's loads and exchange (N = 7168, K = 18432, M = 16: 28.4 us
-    // against 35.7 with 16), where that leaves workgroups enough; 8 waves split the contraction of the others.
-    if (N >= kWideLinear) {
-        if (M <= 16) return launch_linear<2, 1, 4, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-        if (M <= 32) return launch_linear<2, 2, 8, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-        return launch_linear<2, 4, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    switch (linear_shape(M, N)) {
+        case L16x16: return launch_linear<1, 1, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L32x16: return launch_linear<2, 1, 4, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L16x32: return launch_linear<1, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L32x32: return launch_linear<2, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L32x64: return launch_linear<2, 4, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L64x32: return launch_linear<4, 2, 4, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L64x64: break;
     }
-    if (M <= 16) return launch_linear<1, 1, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-    if (M <= 32) return launch_linear<1, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
-    return launch_linear<1, 4, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+    return launch_linear<4, 4, 4, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
 }
