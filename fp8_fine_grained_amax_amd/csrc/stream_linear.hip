@@ -121,7 +121,10 @@ hipError_t launch_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, 
 // with; so the widest that still fills the CUs. Boundaries and estimates from 15 weights (N, K = 1024 to 18432) at 17 to
 // 1024 rows; in us, N x K at M rows:
 //   up to 16 rows   32 columns from N = 4096 on (7168 x 18432, 16: 28.4 against 35.7), 16 below
-//   up to 32 rows   32x32, 16x32 below N = 4096 (7168 x 7168, 32: 14.1 against 21; 2048 x 16384, 32: 22.6 against 18.2)
+//   more rows, as long as a workgroup for every CU holds them: 16x16 (512 x 7168, 128: 6.1; 8.5 with 32x32; 2048 x 16384,
+//                   32: 13.2; 17.9 with 16x32; but 1024 x 1024, 256, four a CU: 5.3 against 4.1)
+//   up to 32 rows   32x32, 16x32 below N = 4096 (7168 x 7168, 32: 14.1 against 21; 3968 x 8192, 32: 11.9 against 14.0 with
+//                   16x16)
 //   more, by the number of 32x32 tiles:
 //     below 384     32x32 (2048 x 16384, 128: 21.1; 28.8 with 32x64)
 //     below 800     32x64 (1024 x 4096, 512: 9.7; 10.5 with 32x32, 11.7 with 64x32)
@@ -134,6 +137,7 @@ int64_t linear_tiles(int64_t M, int64_t N, int cols, int rows) { return ((N + co
 LinearShape linear_shape(int64_t M, int64_t N) {
     const bool wide = N >= 4096;
     if (M <= 16) return wide ? L32x16 : L16x16;
+    if (linear_tiles(M, N, 16, 16) <= 256) return L16x16;
     if (M <= 32) return wide ? L32x32 : L16x32;
     const int64_t small = linear_tiles(M, N, 32, 32), large = linear_tiles(M, N, 64, 64);
     if (small < 384) return L32x32;
@@ -163,7 +167,11 @@ double fg_stream_linear_us(int64_t M, int64_t N, int64_t K) {
 hipError_t fg_launch_stream_linear(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                    int64_t N, int64_t K, const FgEpilogue& e, void* y, int out_bf16, hipStream_t stream) {
     switch (linear_shape(M, N)) {
-        case L16x16: return launch_linear<1, 1, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+        case L16x16:
+            // two steps ahead where a wave has at least four (1 x 2048 x 16384: 10.7 us against 14.7); with one or two the
+            // loads past the end cost 0.2 (16 x 1024 x 1024)
+            if (K >= 4096) return launch_linear<1, 1, 8, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
+            return launch_linear<1, 1, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
         case L32x16: return launch_linear<2, 1, 4, 2>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
         case L16x32: return launch_linear<1, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);
         case L32x32: return launch_linear<2, 2, 8, 1>(xq, sx, wq, sw, M, N, K, e, y, out_bf16, stream);

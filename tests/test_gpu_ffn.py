@@ -120,6 +120,19 @@ def test_linear_small_tiles_exact(M, K, monkeypatch):
     assert torch.equal(y.cpu(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 300, 4224), (16, 77, 8192), (40, 300, 4224), (10, 4100, 384), (30, 3001, 256), (17, 4100, 640),
+                                   (32, 4097, 256), (100, 1030, 640), (333, 515, 1280), (300, 1400, 256), (1000, 1000, 256),
+                                   (999, 1013, 384), (1500, 1024, 256), (1490, 1013, 384), (1985, 770, 128)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_streaming_shapes(M, N, K, dtype):
+    """Every workgroup shape of the kernel that streams the weights, whole and ragged, short and long contractions."""
+    ops = linear_case(M, M, N, K)
+    bias, residual = rand(1, N), rand(2, M, N + 1, dtype=dtype)[:, 1:]
+    y = torch.full((M, N), float("nan"), dtype=dtype, device=device())
+    fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_GELU_TANH, residual=residual, y=y)
+    check_linear(ops, y, "gelu", bias, residual)
+
+
 @pytest.mark.parametrize("M", [1, 16, 64, 65, 256])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_linear_residual_in_place(M, dtype):
