@@ -46,7 +46,10 @@ struct FgResidual8 {
 // consecutive columns a lane. So bias, residual and output are read and written in whole rows, and the
 // accumulators are out of the registers before the activation's variants need any: applied to the
 // accumulators themselves, they spill the 8-wave shapes. With sizes or pointers that forbid 16-byte accesses, a lane
-// takes one element at a time, still along the rows. (m, n): the tile's first row and column.
+// takes one element at a time, still along the rows, eight elements' loads together. Behind a 256 x 288 tile of the training
+// step (M = 4096, N = 18432, K = 7168, power-of-2 scales) 449 us with bias and GELU and 431 with neither, 422 for the
+// Fprop: the waves of a tile reach it together, so nothing hides its VALU work. An odd width costs 512 x 2001 x 2048
+// 26 us instead of 18 on 128 x 128 tiles. (m, n): the tile's first row and column.
 template <int WAVE_N, int MSUB, int NSUB>
 __device__ __forceinline__ void fg_store_epilogue(const FgEpilogue& ep, const v4f (&acc)[MSUB][NSUB], uint8_t* region, int lane,
                                                   int64_t m, int64_t m_end, int64_t n, int64_t N, void* out, int out_bf16) {

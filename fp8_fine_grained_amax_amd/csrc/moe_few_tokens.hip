@@ -13,9 +13,14 @@
 // reads); every workgroup works the slots out for itself and quantizes the activations that it needs as it loads them.
 //
 // For more tokens that work would be done too often, and most columns would stand idle: 64 tokens with 8 choices
-// among 64 experts give each expert 8. Two small launches (5 us each) go between: one quantizes x and writes down for
-// each slot its tokens, closely packed into tiles of 16 (MoePlan), one quantizes the hidden values as MFMA operands in
-// that order. A slot then runs with 1, 2 or 4 token tiles.
+// among 64 experts give each expert 8. Two small launches go between: one quantizes x and writes down for each slot its
+// tokens, closely packed into tiles of 16 (MoePlan), one quantizes the hidden values as MFMA operands in that order. A
+// slot then runs with 1, 2 or 4 token tiles.
+//
+// Measured, H = 7168, I = 2048. One token, 8 experts: up 44.4 us (235 MB, 5.3 TB/s), down 28.1 (117 MB, 4.2 TB/s; 224
+// workgroups for 256 CUs, and the experts' list before the first load). 64 tokens, 8 choices of 64 experts, 16 of them
+// here: plan 8.1, up 87 (470 MB, 5.4 TB/s), quantize 4.8, down 48.6 (235 MB, 4.8 TB/s); with the fused launches 162 in
+// all instead of 147.
 #include "ffn_launch.h"
 #include "host_util.h"
 #include "weight_stream.h"

@@ -8,7 +8,9 @@ namespace {
 
 // ---------------------------------------------------------------------------------------------------------
 // A Linear of few rows: y = act(x . W^T + bias) + residual. A workgroup owns 16 RT output columns and 16 NT
-// tokens; its waves split the contraction.
+// tokens; its waves split the contraction, so that a CU has several K blocks' loads in flight and no loop is long.
+// N = 7168, K = 18432, 16 rows: 26.6 us for 133 MB (5.0 TB/s). One row, N = K = 1024: 3.5 us, the latency of a load, an
+// MFMA and the join. Many rows move the operands through L2 instead: 300 rows, N = 2001, K = 2048: 11.8 us.
 // ---------------------------------------------------------------------------------------------------------
 template <int RT, int NT, int NW, int DEPTH>
 __global__ __launch_bounds__(NW * 64) void fg_stream_linear_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx,

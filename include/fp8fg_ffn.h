@@ -36,7 +36,8 @@ typedef enum { FG_ACT_NONE = 0, FG_ACT_RELU = 1, FG_ACT_GELU_TANH = 2, FG_ACT_SI
  *   K % 128 == 0; any M, N >= 0 (M == 0 or N == 0: no-op; K == 0: act(bias) + residual). xq, wq, y 16-byte
  *   aligned; sx, sw 4-byte aligned; bias and residual aligned to their elements. The size limits of
  *   fg_fp8_gemm_fprop hold. The problem's sizes choose between a kernel that streams the weights past
- *   few rows and the GEMM tiles (128x128 or the Fprop's); the streaming kernel adds a row's blocks up in another order.
+ *   few rows and the GEMM tiles (128x128 or the Fprop's); the streaming kernel adds a row's blocks up in another order,
+ *   and it and the 128x128 tiles apply power-of-2 scales as any others, so sums may differ in their last bits.
  *   FG_GEMM_TILE forces a tile, as there; 128x128 is one of them here. */
 fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
                                      int64_t N, int64_t K, const void* bias, fg_out_dtype bias_type, fg_act act,
