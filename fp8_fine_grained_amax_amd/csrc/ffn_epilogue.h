@@ -47,8 +47,9 @@ struct FgResidual8 {
 // accumulators are out of the registers before the activation's variants need any: applied to the
 // accumulators themselves, they spill the 8-wave shapes. With sizes or pointers that forbid 16-byte accesses, a lane
 // takes one element at a time, still along the rows, eight elements' loads together. Behind a 256 x 288 tile of the training
-// step (M = 4096, N = 18432, K = 7168, power-of-2 scales) 449 us with bias and GELU and 431 with neither, 422 for the
-// Fprop: the waves of a tile reach it together, so nothing hides its VALU work. An odd width costs 512 x 2001 x 2048
+// step (M = 4096, N = 18432, K = 7168, power-of-2 scales) 449 us with bias and GELU and 434 with neither, 429 for the
+// Fprop: the waves of a tile reach it together, so nothing hides its VALU work (half of it the exponential and the
+// reciprocal). An odd width costs 512 x 2001 x 2048
 // 26 us instead of 18 on 128 x 128 tiles. (m, n): the tile's first row and column.
 template <int WAVE_N, int MSUB, int NSUB>
 __device__ __forceinline__ void fg_store_epilogue(const FgEpilogue& ep, const v4f (&acc)[MSUB][NSUB], uint8_t* region, int lane,
@@ -56,9 +57,9 @@ __device__ __forceinline__ void fg_store_epilogue(const FgEpilogue& ep, const v4
     constexpr int CH = WAVE_N / 4, OCT = WAVE_N / 8;               // 16-byte chunks and groups of eight in a row
     constexpr int STEPS = 32 * OCT / 64, GROUP = STEPS % 4 == 0 ? 4 : 3;
     static_assert(STEPS % GROUP == 0 && MSUB % 2 == 0, "whole groups of rows");
-    // 64 columns: chunk c of row r at c ^ (r % 16), free of conflicts both ways. 144: rows of 576 bytes shift by
-    // themselves.
-    auto chunk = [&](int r, int c) { return region + (r * CH + (WAVE_N == 64 ? c ^ (r & 15) : c)) * 16; };
+    // 64 columns: chunk c of row r at c ^ (r % 16), free of conflicts both ways. 144: rows of 576 bytes shift by 16 banks,
+    // so four rows apart meet, which the chunk's two low bits undo when it is written.
+    auto chunk = [&](int r, int c) { return region + (r * CH + (WAVE_N == 64 ? c ^ (r & 15) : c ^ ((r >> 2) & 3))) * 16; };
     const int lrow = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int h = 0; h < MSUB / 2; h++) {

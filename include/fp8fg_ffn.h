@@ -50,7 +50,7 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
  *   zq  u8 [rows][W], sz f32 [W/128][rows]: fg_quantize_act_1x128(z, FG_ALONG_COLS, mode), bit for bit.
  *   aq  u8 [rows][F], sa f32 [F/128][rows]: a in the same tiling, the next Linear's input.
  *   F % 128 == 0, F <= 2^23, rows <= 2^25, F * ceil(rows / 32) < 2^31. z, zq, aq 16-byte aligned; ld_z % 8 == 0; sz, sa 4-byte aligned.
- *   rows == 0 or F == 0 is a no-op. */
+ *   rows == 0 or F == 0 is a no-op. Outputs must not overlap z or each other. */
 fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t ld_z, fg_act act, int gated,
                                 fg_scale_mode mode, uint8_t* zq, float* sz, uint8_t* aq, float* sa, hipStream_t stream);
 
@@ -70,7 +70,8 @@ fg_status fg_act_checkpoint_fwd(const void* z, int64_t rows, int64_t F, int64_t 
  *            that may run at the same time need workspaces of their own.
  *   F % 128 == 0; rows % 128 == 0 where a tiling along the rows is asked for, any rows otherwise; F and ld_da at most
  *   2^23, rows at most 2^25, F * ceil(rows / 128) < 2^30. zq, da, dzq_cols, dzq_rows, aq_rows 16-byte aligned, ld_da a multiple of 16 bytes; the fp32 outputs and sz 4-byte aligned.
- *   rows == 0 or F == 0: no-op, but for dbias, which becomes 0. */
+ *   rows == 0 or F == 0: no-op, but for dbias, which becomes 0. Outputs and workspace must not overlap the inputs or each
+ *   other. */
 int64_t fg_act_checkpoint_bwd_workspace(int64_t rows, int64_t F, int gated);
 fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* da, fg_out_dtype da_type, int64_t ld_da,
                                 int64_t rows, int64_t F, fg_act act, int gated, fg_scale_mode mode, uint8_t* dzq_cols,
