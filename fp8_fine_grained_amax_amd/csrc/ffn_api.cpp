@@ -106,8 +106,9 @@ fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* 
 }
 
 int64_t fg_moe_few_tokens_workspace(int64_t T, int32_t topk, int64_t H, int64_t I) {
-    if (T < 0 || T > kMaxTokens || topk < 1 || topk > kMaxTopk || H < 0 || H > kMaxExpertDim || I < 0 || I > kMaxExpertDim)
-        return 0;
+    if (T < 0 || T > kMaxTokens || topk < 1 || topk > kMaxTopk || H < 0 || H > kMaxExpertDim || I < 0 || I > kMaxExpertDim ||
+        H % 128 != 0 || I % 128 != 0)
+        return 0;      // sizes that fg_moe_few_tokens refuses
     return fg_moe_workspace_bytes(T, topk, H, I);
 }
 

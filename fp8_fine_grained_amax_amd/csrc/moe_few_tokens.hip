@@ -700,8 +700,8 @@ constexpr int kDownWaves = 8;
 // leave half of the CUs without one, and no more than leave each wave four steps. Joining their sums costs another
 // launch of 4.5 us. (64 tokens, 64 experts, H = 2048, I = 1024, 64 column blocks: 105 us, split 54 with the join.)
 int down_splits(int64_t blocks, int64_t slots, int64_t nkb) {
+    if (blocks < 1 || blocks > 128) return 1;
     const int64_t by_steps = slots * nkb / (4 * kDownWaves), by_cus = 512 / blocks;
-    if (blocks > 128) return 1;
     const int64_t s = by_steps < by_cus ? by_steps : by_cus;
     return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }

@@ -90,7 +90,7 @@ fg_status fg_act_checkpoint_bwd(const uint8_t* zq, const float* sz, const void* 
  *   w2q  u8 [E][H][I], s2 f32 [E][H/128][I/128].
  *   act_scales  the scale mode of the two activations; the weights' scales may be any fp32 in both.
  *   workspace   fg_moe_few_tokens_workspace(T, topk, H, I) bytes, 16-byte aligned; calls that may run at the same
- *               time need workspaces of their own.
+ *               time need workspaces of their own. The size of a T, topk, H or I that is refused here is 0.
  *   y    [T][H] f32 or bf16, row stride ld_y.
  *   0 <= T <= 64, 1 <= topk <= 32, 1 <= E <= 2048, H % 128 == 0, I % 128 == 0, H and I at most 2^20, I * min(E, T * topk) <
  *   2^29. x, w1q, w2q, y
