@@ -23,13 +23,12 @@
 // all instead of 147.
 #include "ffn_launch.h"
 #include "host_util.h"
+#include "moe_workspace.h"
 #include "weight_stream.h"
 
 #include <type_traits>
 
 namespace {
-
-constexpr int kWords = 64;          // bitmap words: 2048 experts
 
 // The chosen experts as a bitmap in LDS with the count of the ones before each word; returns how many there
 // are. Ends with a barrier. `ids` is a copy of the choices in LDS.
@@ -363,22 +362,6 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_kernel(FgMoe p, const flo
 
 // ---- more tokens ------------------------------------------------------------------------------------------
 
-// The slots as the planning launch writes them down for the others, and the activations' codes. A slot's tokens
-// have consecutive places, 16 to a tile; the places of a slot's last tile that have no token hold token and pair -1.
-struct MoePlan {
-    int* used;            // number of slots
-    int* list;            // [slots] experts
-    int* base;            // [slots + 1] first tile
-    int* place;           // [T * topk] place of a choice, or -1
-    int* token;           // [tiles * 16]
-    int* pair;            // [tiles * 16] choice: token * topk + number
-    float* weight;        // [tiles * 16] routing weight
-    uint8_t* xq;          // [T][H] codes
-    float* sx;            // [H / 128][T]
-    uint8_t* hq;          // [tiles][I / 128] operand blocks
-    float* sh;
-};
-
 constexpr int kMaxPairs = 64 * 32;
 
 // The last workgroup writes the slots down; the others quantize x.
@@ -668,10 +651,6 @@ __global__ __launch_bounds__(NW * 64) void fg_moe_down_many_kernel(FgMoe p, MoeP
 
 // ---- launches ---------------------------------------------------------------------------------------------
 
-// A model narrow enough to leave CUs without a column block, and with steps enough, has each block's shared between up
-// to 8 workgroups.
-constexpr int kMaxSplits = 8;
-
 // Joins the partial sums of the down-projection's workgroups, in order.
 __global__ __launch_bounds__(256) void fg_moe_join_kernel(FgMoe p, const float* __restrict__ partial, int splits) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, tok = id / (p.H / 4), n = id % (p.H / 4) * 4;
@@ -692,64 +671,6 @@ template <class Kernel>
 hipError_t raise_lds(Kernel kern, int bytes, std::atomic<uint64_t>& done) {
     return bytes > 65536 ? fg_set_lds_limit_once((const void*)kern, 128 * 1024, done) : hipSuccess;
 }
-
-constexpr int64_t kFusedTokens = 16;   // up to here the activations are quantized inside the two products
-constexpr int kDownWaves = 8;
-
-// Workgroups that share a column block of the down-projection: as many as give every CU two, where the blocks alone
-// leave half of the CUs without one, and no more than leave each wave four steps. Joining their sums costs another
-// launch of 4.5 us. (64 tokens, 64 experts, H = 2048, I = 1024, 64 column blocks: 105 us, split 54 with the join.)
-int down_splits(int64_t blocks, int64_t slots, int64_t nkb) {
-    if (blocks < 1 || blocks > 128) return 1;
-    const int64_t by_steps = slots * nkb / (4 * kDownWaves), by_cus = 512 / blocks;
-    const int64_t s = by_steps < by_cus ? by_steps : by_cus;
-    return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
-}
-// 16-row tiles of the down-projection's workgroups: two share the tokens' operands (with up to 16 tokens only where that
-// leaves workgroups enough, or they are split).
-int down_tiles(int64_t T, int64_t H, int64_t slots, int64_t I) {
-    return T > kFusedTokens || H >= 4096 || down_splits(H / 32, slots, I / BK) > 1 ? 2 : 1;
-}
-
-int64_t pad16(int64_t bytes) { return (bytes + 15) / 16 * 16; }
-
-// Workspace: the hidden values in fp32; partial sums of a split down-projection; for more than 16 tokens also the plan and
-// the activations' codes. A call's slots are at most its choices (and fewer are never split more often); a slot's tokens
-// fill all its tiles but the last.
-struct MoeWorkspace {
-    int64_t rows, slots, tiles, partial, plan, xq, sx, hq, sh, bytes;
-    MoeWorkspace(int64_t T, int topk, int64_t H, int64_t I) {
-        rows = T * topk;
-        slots = rows < 32 * kWords ? rows : 32 * kWords;
-        tiles = slots + rows / 16;
-        partial = rows * I * 4;
-        const int splits = H == 0 ? 1 : down_splits(H / (16 * down_tiles(T, H, slots, I)), slots, I / BK);
-        bytes = partial + (splits > 1 ? splits * T * H * 4 : 0);
-        plan = xq = sx = hq = sh = bytes;
-        if (T > kFusedTokens) {
-            xq = plan + pad16(4 * (2 + 2 * slots + rows + 3 * 16 * tiles));
-            sx = xq + T * H;
-            hq = sx + pad16(T * (H / BK) * 4);
-            sh = hq + tiles * 16 * I;
-            bytes = sh + tiles * 16 * (I / BK) * 4;
-        }
-    }
-    MoePlan of(uint8_t* ws) const {
-        MoePlan m{};
-        m.used = (int*)(ws + plan);
-        m.list = m.used + 1;
-        m.base = m.list + slots;
-        m.place = m.base + slots + 1;
-        m.token = m.place + rows;
-        m.pair = m.token + 16 * tiles;
-        m.weight = (float*)(m.pair + 16 * tiles);
-        m.xq = ws + xq;
-        m.sx = (float*)(ws + sx);
-        m.hq = ws + hq;
-        m.sh = (float*)(ws + sh);
-        return m;
-    }
-};
 
 template <int RG, int NW, int DEPTH>
 hipError_t launch_up(const FgMoe& p, float* h, int64_t slots, hipStream_t stream) {
@@ -790,8 +711,9 @@ hipError_t fg_launch_moe_few_tokens(const FgMoe& p, hipStream_t stream) {
     const MoeWorkspace at(p.T, p.topk, p.H, p.I);
     uint8_t* ws = (uint8_t*)p.workspace;
     float *h = (float*)ws, *partial = (float*)(ws + at.partial);
-    const int64_t slots = at.rows < p.E ? at.rows : p.E;
-    const int tiles = down_tiles(p.T, p.H, slots, p.I), splits = down_splits(p.H / (16 * tiles), slots, p.I / BK);
+    const MoeLaunch shape(p.T, p.topk, p.E, p.H, p.I);
+    const int64_t slots = shape.slots;
+    const int tiles = shape.tiles, splits = shape.splits;
     hipError_t e = hipSuccess;
     if (p.T <= kFusedTokens) {
         // 32 gate and 32 up rows a workgroup (they share the token's quantization) where that leaves three quarters of the CUs

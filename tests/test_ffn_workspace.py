@@ -1,7 +1,11 @@
-"""Workspace sizes of the mixture of experts, asked of the library itself for any width."""
+"""Workspace sizes of the mixture of experts for any width: asked of the library itself, and their arithmetic under
+sanitizers."""
 import os
+import shutil
 import subprocess
 import sys
+
+import pytest
 
 import fp8_fine_grained_amax_amd as fg
 
@@ -29,3 +33,15 @@ def test_moe_workspace_of_any_width():
         build.build()
     r = subprocess.run([sys.executable, "-c", ANY_WIDTH], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "every width asked" in r.stdout, (r.returncode, r.stdout, r.stderr)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_moe_workspace_under_sanitizers(tmp_path):
+    exe = tmp_path / "moe_workspace_driver"
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
+                        "-I", os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc"),
+                        os.path.join(ROOT, "tests", "moe_workspace_driver.cpp"), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "runtime error" not in r.stderr, r.stdout + r.stderr
+    assert "moe workspace driver done" in r.stdout
