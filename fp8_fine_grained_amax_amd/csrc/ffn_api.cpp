@@ -2,11 +2,12 @@
 // caller's stream. Declarations, layouts and error behaviour: include/fp8fg_ffn.h.
 #include "fp8fg_ffn.h"
 
+#include <stdlib.h>
+
 #include "ffn_launch.h"
 
 namespace {
 
-constexpr int64_t kMaxGrid = 2147483647LL;
 constexpr int64_t kMaxThreads = (1LL << 32) - 1; // of a launch along one dimension
 constexpr int64_t kMaxContraction = 1LL << 24;   // as in the other GEMMs: 32-bit operand offsets
 constexpr int64_t kMaxCols = 1LL << 23;          // 32-bit offsets inside a 128-row block of up to 2 F codes or F fp32 values
@@ -24,6 +25,12 @@ bool valid_type(int o) { return o == FG_OUT_F32 || o == FG_OUT_BF16; }
 bool valid_act(int a) { return a >= FG_ACT_NONE && a <= FG_ACT_SILU; }
 int64_t cdiv(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 bool prod_over(int64_t a, int64_t b, int64_t limit) { return a != 0 && b > limit / a; }
+// Whether a Linear's launch on GEMM tiles would have too many threads: 256 to 128x128 outputs. The larger shapes are taken
+// where they need no more; a forced one may need up to 768 to 256x192.
+bool linear_threads_over(int64_t M, int64_t N) {
+    return prod_over(cdiv(M, 128), cdiv(N, 128), kMaxThreads / 256) ||
+           (getenv("FG_GEMM_TILE") && prod_over(cdiv(M, 256), cdiv(N, 192), kMaxThreads / 768));
+}
 uintptr_t size_of(int type) { return type == FG_OUT_F32 ? 4 : 2; }
 
 }  // namespace
@@ -41,8 +48,7 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
     if (!y || (K > 0 && (!xq || !sx || !wq || !sw))) return FG_ERR_INVALID_ARG;
     // y as its own residual is read where it is written; with another type or stride it would be overwritten first
     if (residual == y && (residual_type != out || ld_res != N)) return FG_ERR_INVALID_ARG;
-    if (K % 128 != 0 || K > kMaxContraction || prod_over(cdiv(M, 256), cdiv(N, 128), kMaxGrid) ||
-        (residual && ld_res > kMaxStride))
+    if (K % 128 != 0 || K > kMaxContraction || (residual && ld_res > kMaxStride) || linear_threads_over(M, N))
         return FG_ERR_UNSUPPORTED_SHAPE;
     if (!aligned(xq, 16) || !aligned(wq, 16) || !aligned(y, 16) || !aligned(sx, 4) || !aligned(sw, 4) ||
         (bias && !aligned(bias, size_of(bias_type))) || (residual && !aligned(residual, size_of(residual_type))))

@@ -34,8 +34,9 @@ typedef enum { FG_ACT_NONE = 0, FG_ACT_RELU = 1, FG_ACT_GELU_TANH = 2, FG_ACT_SI
  *   y         [M][N] f32 or bf16 (row stride N). The sum, bias, activation and residual are fp32, and the
  *             result is rounded once, when it is stored.
  *   K % 128 == 0; any M, N >= 0 (M == 0 or N == 0: no-op; K == 0: act(bias) + residual). xq, wq, y 16-byte
- *   aligned; sx, sw 4-byte aligned; bias and residual aligned to their elements. The size limits of
- *   fg_fp8_gemm_fprop hold. The problem's sizes choose between a kernel that streams the weights past
+ *   aligned; sx, sw 4-byte aligned; bias and residual aligned to their elements. K <= 2^24;
+ *   ceil(M / 128) * ceil(N / 128) < 2^24, and with FG_GEMM_TILE also ceil(M / 256) * ceil(N / 192) <= 5592405 (a launch
+ *   has less than 2^32 threads). The problem's sizes choose between a kernel that streams the weights past
  *   few rows and the GEMM tiles (128x128 or the Fprop's); the streaming kernel adds a row's blocks up in another order,
  *   and it and the 128x128 tiles apply power-of-2 scales as any others, so sums may differ in their last bits.
  *   FG_GEMM_TILE forces a tile, as there; 128x128 is one of them here. */

@@ -1,0 +1,55 @@
+"""The Linear's choice between its two kernels, and the sizes it refuses, without a GPU (the launchers are stubs)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, SHAPE = 0, 2
+
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                                reason="needs g++ and the HIP headers")
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("linear") / "driver")
+    csrc = os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I",
+                        os.path.join(ROOT, "include"), "-I", csrc, os.path.join(csrc, "ffn_api.cpp"),
+                        os.path.join(ROOT, "tests", "linear_dispatch_driver.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+    def ask(stream_us, tiles_us, M, N, K, tile=None):
+        env = {k: v for k, v in os.environ.items() if k != "FG_GEMM_TILE"}
+        if tile:
+            env["FG_GEMM_TILE"] = tile
+        r = subprocess.run([exe], input=f"{stream_us} {tiles_us} {M} {N} {K}\n", capture_output=True, text=True, timeout=60, env=env)
+        assert r.returncode == 0, r.stderr
+        status, launched = r.stdout.split()
+        return int(status), launched
+    return ask
+
+
+@pytest.mark.parametrize("M,N,K,fits", [
+    (1 << 31, 1, 0, False),                            # 2^24 workgroups of 256 threads
+    ((1 << 31) - 128, 1, 0, True),
+    ((1 << 31) - 127, 128, 128, False),
+    (1, 1 << 31, 128, False),
+    (128, (1 << 31) - 128, 128, True),
+    (1 << 31, 1 << 31, 128, False),
+    (5592405 * 256, 192, 0, False),                    # two columns of 128x128
+    (5592405 * 256 + 1, 129, 0, False),
+    (5592405 * 256 + 1, 128, 0, True),                 # one column
+    (1 << 62, 1, 128, False),
+    (1, 1 << 62, 0, False),
+])
+def test_launches_past_32_bits_of_threads_are_refused(driver, M, N, K, fits):
+    assert driver(2, 1, M, N, K) == ((OK, "tiles") if fits else (SHAPE, "-"))
+
+
+def test_a_forced_tile_is_held_to_its_own_threads(driver):
+    M = 5592405 * 256 + 1
+    assert driver(2, 0, M, 128, 0, tile="256x192") == (SHAPE, "-")
+    assert driver(2, 0, M - 1, 128, 0, tile="256x192") == (OK, "tiles")
