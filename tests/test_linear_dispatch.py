@@ -53,3 +53,12 @@ def test_a_forced_tile_is_held_to_its_own_threads(driver):
     M = 5592405 * 256 + 1
     assert driver(2, 0, M, 128, 0, tile="256x192") == (SHAPE, "-")
     assert driver(2, 0, M - 1, 128, 0, tile="256x192") == (OK, "tiles")
+
+
+def test_no_estimate_beats_the_memory(tmp_path):
+    exe = str(tmp_path / "estimates")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc"),
+                        os.path.join(ROOT, "tests", "stream_estimate_driver.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
