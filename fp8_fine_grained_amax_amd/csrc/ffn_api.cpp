@@ -15,7 +15,12 @@ constexpr int64_t kMaxRows = 1LL << 25;          // and inside a 128-column bloc
 constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxExpertDim = 1LL << 20;
 constexpr int64_t kMaxTokens = 64;
-constexpr int64_t kMaxStreamRows = 4096;         // a grid of 64 blocks of rows; its estimate lies far above the tiles' by then
+constexpr int64_t kMaxStreamRows = 65535 * 16;   // a grid's y, of 16 rows at least
+// Past 4096 rows only weights of few columns are streamed. There the estimates were measured on both sides (4097 to
+// 262144 rows, K = 128 to 16384), and nothing streams for more than 6% longer than the tiles take: in us, streaming and on
+// tiles, 8192 rows of 64 x 7168 21 and 45, of 256 x 512 9.2 and 8.7; 65536 of 256 x 1024, which go to the tiles, 69 and 29.
+// On more columns they put the tiles too far behind: 5000 rows of 512 x 2048 count 20.2 and 20.4 and take 22.2 and 16.7.
+constexpr int64_t kFewCols = 256, kFewColsRows = 4096;
 constexpr int64_t kMaxStreamCols = 1LL << 26;    // kMaxThreads: 512 threads to 16 columns
 constexpr int kMaxTopk = 32, kMaxExperts = 2048;
 
@@ -58,7 +63,8 @@ fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const u
     const FgEpilogue e{bias, residual, ld_res, bias && bias_type == FG_OUT_BF16,
                        residual && residual_type == FG_OUT_BF16, (int)act, vector_ok};
     const int bf16 = out == FG_OUT_BF16;
-    if (M <= kMaxStreamRows && N <= kMaxStreamCols && fg_stream_linear_us(M, N, K) <= fg_gemm_epilogue_us(M, N, K))
+    const bool may_stream = M <= kMaxStreamRows && N <= kMaxStreamCols && (M <= kFewColsRows || N <= kFewCols);
+    if (may_stream && fg_stream_linear_us(M, N, K) <= fg_gemm_epilogue_us(M, N, K))
         return fg_status_from_hip(fg_launch_stream_linear(xq, sx, wq, sw, M, N, K, e, y, bf16, stream));
     return fg_status_from_hip(
         fg_launch_gemm_fprop_epilogue(xq, sx, wq, sw, M, N, K, e, y, bf16, scales == FG_SCALE_POW2, stream));

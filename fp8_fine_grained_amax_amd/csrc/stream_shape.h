@@ -36,7 +36,9 @@ inline LinearShape linear_shape(int64_t M, int64_t N) {
 
 // Estimated time in us: launch and latency, then the larger of the tiles' K steps and the weights' bytes from HBM (slower
 // the more rows share the waits), and no less than reading both operands takes: the activations are the larger one where
-// the output is narrow (N = 8, K = 16384, in us: 4096 rows 14.3, estimated 14.7; 16384 rows 48.9 and 48.2).
+// the output is narrow (N = 8, K = 16384, in us: 4096 rows 14.3, estimated 14.7; 16384 rows 48.9 and 48.2). Many 64x32
+// tiles on a short contraction pay for their joins and stores as well (K = 128, in us: 8192 x 1024 15.5 and on tiles 10.3, where the
+// steps alone would be 6.9; K = 512: 1024 x 2944 10.6 and 9.0, where they would be 8.4).
 inline double stream_linear_us(int64_t M, int64_t N, int64_t K) {
     const double steps = (double)(K / 128), bytes = (double)N * (double)K;
     auto larger = [](double a, double b) { return a > b ? a : b; };
@@ -47,7 +49,7 @@ inline double stream_linear_us(int64_t M, int64_t N, int64_t K) {
         case L16x32: us = 4.0 + bytes / 3.0e6; break;
         case L32x32: us = 3.5 + larger(0.6e-3 * steps * (double)linear_tiles(M, N, 32, 32), bytes / 3.7e6); break;
         case L32x64: us = 3.5 + 1.0e-3 * steps * (double)linear_tiles(M, N, 32, 64) + bytes / 17e6; break;
-        case L64x32: us = 3.5 + larger(0.83e-3 * steps * (double)linear_tiles(M, N, 64, 32), bytes / 2.5e6); break;
+        case L64x32: us = 3.5 + larger(larger(0.83e-3 * steps, 2.3e-3 + 0.62e-3 * steps) * (double)linear_tiles(M, N, 64, 32), bytes / 2.5e6); break;
         case L64x64: us = 5.0 + larger(0.52 * steps, bytes / 3.0e6); break;
     }
     return larger(us, 3.5 + (bytes + (double)M * (double)K) / 6.0e6);

@@ -4,7 +4,7 @@ import torch
 
 import fp8_fine_grained_amax_amd as fg
 from tests.gpu_util import device
-from tests.test_gpu_ffn import experts, rand, routing
+from tests.test_gpu_ffn import check_linear, experts, linear_case, rand, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +22,15 @@ def test_moe_width_that_is_no_multiple_of_a_tile_is_refused(T, H, given):
     with pytest.raises(fg.Fp8fgError, match="shape"):
         fg.fg_moe_few_tokens(rand(2, T, H), ids, weights, w1, s1, w2, s2, workspace=ws)
     assert fg.lib().fg_last_hip_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(4097, 64, 1024), (5000, 17, 640), (8192, 130, 512), (20001, 8, 1152), (16384, 200, 128),
+                                   (70001, 3, 256), (65535 * 16, 1, 128), (65535 * 16 + 1, 1, 128)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_many_rows_on_a_narrow_weight(M, N, K, dtype):
+    """A router's projection in training: more rows than 4096 on a few columns."""
+    ops = linear_case(M, M, N, K)
+    bias, residual = rand(1, N), rand(2, M, N, dtype=dtype)
+    y = torch.full((M, N), float("nan"), dtype=dtype, device=device())
+    fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_SILU, residual=residual, y=y)
+    check_linear(ops, y, "silu", bias, residual)

@@ -55,6 +55,21 @@ def test_a_forced_tile_is_held_to_its_own_threads(driver):
     assert driver(2, 0, M - 1, 128, 0, tile="256x192") == (OK, "tiles")
 
 
+@pytest.mark.parametrize("M", [1, 4096, 4097, 8192, 100000, 65535 * 16])
+def test_the_estimates_choose_at_any_number_of_rows(driver, M):
+    assert driver(1, 2, M, 64, 7168) == (OK, "stream")
+    assert driver(2, 1, M, 64, 7168) == (OK, "tiles")
+
+
+@pytest.mark.parametrize("M,N", [(1, 18432), (4096, 18432), (4096, 257), (4097, 257), (8192, 512)])
+def test_many_rows_and_columns_go_to_the_tiles(driver, M, N):
+    assert driver(1, 2, M, N, 2048) == (OK, "stream" if M <= 4096 else "tiles")
+
+
+def test_rows_past_a_grid_go_to_the_tiles(driver):
+    assert driver(1, 2, 65535 * 16 + 1, 64, 7168) == (OK, "tiles")
+
+
 def test_no_estimate_beats_the_memory(tmp_path):
     exe = str(tmp_path / "estimates")
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc"),
