@@ -1,9 +1,11 @@
-"""Build libfp8fg.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Build libfp8fg.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree, and where torch and g++ are there _ffn.so too.
 
 Flags: -O3, no fast-math, no FP contraction (every FMA in the kernels is written explicitly),
 packed-FP32 instructions disabled, IEEE fp32 division (HIP's default correctly rounded divide).
 """
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 
@@ -55,11 +57,27 @@ def build(verbose: bool = False, extra=()) -> str:
         sys.stderr.write(r.stderr + "\n")
         raise RuntimeError("the built library does not load: " + r.stderr.strip().splitlines()[-1])
     os.replace(LIB + ".tmp", LIB)
-    build_ffn_module(verbose)
+    missing = ffn_module_needs()
+    if missing:
+        # an older binding may not fit the new library; without one, its functions raise at their first call
+        if os.path.exists(FFN_MODULE):
+            os.remove(FFN_MODULE)
+        sys.stderr.write(f"{os.path.basename(FFN_MODULE)}, the Python binding of the feed-forward operators, is not built: "
+                         f"it needs {missing}; the C library is complete\n")
+    else:
+        build_ffn_module(verbose)
     return LIB
 
 
 FFN_MODULE = os.path.join(HERE, "_ffn.so")
+
+
+def ffn_module_needs() -> str:
+    """What is missing here of what build_ffn_module takes; the C library and its callers take hipcc alone."""
+    missing = [] if importlib.util.find_spec("torch") else ["torch"]
+    if not shutil.which("g++"):
+        missing.append("g++")
+    return " and ".join(missing)
 
 
 def build_ffn_module(verbose: bool = False) -> str:
