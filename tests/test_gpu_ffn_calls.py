@@ -4,7 +4,7 @@ import torch
 
 import fp8_fine_grained_amax_amd as fg
 from tests.gpu_util import device
-from tests.test_gpu_ffn import check_linear, experts, linear_case, rand, routing
+from tests.test_gpu_ffn import check_linear, check_moe, experts, linear_case, rand, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,15 @@ def test_linear_many_rows_on_a_narrow_weight(M, N, K, dtype):
     y = torch.full((M, N), float("nan"), dtype=dtype, device=device())
     fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_SILU, residual=residual, y=y)
     check_linear(ops, y, "silu", bias, residual)
+
+
+@pytest.mark.parametrize("T", [1, 2, 9, 16])
+@pytest.mark.parametrize("H,I,E,topk", [(4096, 128, 3, 2), (4224, 256, 4, 3), (5120, 1152, 4, 4), (8192, 384, 2, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_moe_wide_layers_for_few_tokens(T, H, I, E, topk, dtype):
+    """From 4096 columns on the down-projection has two 16-column tiles a workgroup and is not split."""
+    w = experts(H + E, E, H, I)
+    x = rand(T, T, H)
+    ids, weights = routing(T + H, T, topk, E + 1, E)
+    y = fg.fg_moe_few_tokens(x, ids, weights, *w, out_dtype=dtype)
+    check_moe(y, (x, ids, weights, *w), "silu", False)
