@@ -66,7 +66,7 @@ __device__ __forceinline__ float rows_sum(float v) {
 // Forward. As in the 1x128 quantizer: a tile of z is 256 B = 16 lanes x 16 B, one DPP row, and a 256-thread
 // workgroup covers 16 rows of one 128-column group per slot. The checkpoint's codes come from the bf16 bits
 // of z (bit for bit the quantizer's), a from the same registers. Bound by HBM: 4096 rows, F = 18432, gated SiLU, 102.5 us
-// for 536 MB (5.2 TB/s; a copy runs at 4.7). Two slots a thread keep 64 bytes of gated loads in flight. 7 rows of
+// for 536 MB (5.2 TB/s; a copy of 2 GiB runs at 4.7). Two slots a thread keep 64 bytes of gated loads in flight. 7 rows of
 // F = 2048 take 4.0 us, all latency.
 // ------------------------------------------------------------------------------------------------
 template <int ACT, bool GATED, int UNROLL>
@@ -139,7 +139,9 @@ __global__ __launch_bounds__(256) void fg_act_fwd_kernel(const uint16_t* __restr
 // Addresses are a wave-uniform base and a 32-bit lane offset (the host bounds widths and strides for it).
 // Measured: gated SiLU, 4096 x 18432, FP32 da, every output but the bias gradient: 195 us for 847 MB (4.3 TB/s; 326 without
 // the tile ahead, with the maxima in DPP steps across rows and 64-bit offsets); GELU, 8192 x 7168, bf16 da, every output:
-// 85 us with the sum below for 360 MB.
+// 83 to 86 us with the sum below for 360 MB. One tile alone takes 7.3 us with every output (2.9 for the identity and the
+// column codes), 16 of them 8.2 to 9.1: with few tiles the time is a workgroup's own work. A gated launch's 257th tile is
+// a second one for its CU: 256 tiles 14.6 us, 257 19.3, 512 26.5.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 512, kBwdWaves = kBwdThreads / 64;
 

@@ -1522,7 +1522,8 @@ hipError_t launch_wide(const GemmParams& p, unsigned grid, hipStream_t stream) {
 // The Fprop with its epilogue picks among the Fprop's shapes as fg_launch_gemm_fprop does, and takes the 128 x 128 tiles
 // where they are estimated to end sooner. Time of a K step in us with FP32 scales, while the tiles fill less than
 // a round and more than half of one (M = 16 to 2048, N, K = 1024 to 18432, 66 problems; the 128 x 128 steps with
-// one and with two workgroups a CU).
+// one and with two workgroups a CU). They choose for power-of-2 scales too, which make the larger shapes up to 14% faster: at
+// 384 to 2048 rows of 7168 x 7168 and four other problems the fastest shape is the same in both modes.
 constexpr double kStepMid[2] = {0.74, 0.80}, kStepMid2[2] = {0.90, 1.20};
 constexpr double kStep12[2] = {1.50, 1.68}, kStep8[2] = {1.65, 1.86}, kStepWide[2] = {1.85, 2.05};
 

@@ -37,7 +37,7 @@ typedef enum { FG_ACT_NONE = 0, FG_ACT_RELU = 1, FG_ACT_GELU_TANH = 2, FG_ACT_SI
  *   aligned; sx, sw 4-byte aligned; bias and residual aligned to their elements. K <= 2^24;
  *   ceil(M / 128) * ceil(N / 128) < 2^24, and with FG_GEMM_TILE also ceil(M / 256) * ceil(N / 192) <= 5592405 (a launch
  *   has less than 2^32 threads). The problem's sizes choose between a kernel that streams the weights past
- *   few rows and the GEMM tiles (128x128 or the Fprop's); the streaming kernel adds a row's blocks up in another order,
+ *   the rows, for few rows or few columns, and the GEMM tiles (128x128 or the Fprop's); the streaming kernel adds a row's blocks up in another order,
  *   and it and the 128x128 tiles apply power-of-2 scales as any others, so sums may differ in their last bits.
  *   FG_GEMM_TILE forces a tile, as there; 128x128 is one of them here. */
 fg_status fg_fp8_gemm_fprop_epilogue(const uint8_t* xq, const float* sx, const uint8_t* wq, const float* sw, int64_t M,
