@@ -46,3 +46,28 @@ def test_moe_wide_layers_for_few_tokens(T, H, I, E, topk, dtype):
     ids, weights = routing(T + H, T, topk, E + 1, E)
     y = fg.fg_moe_few_tokens(x, ids, weights, *w, out_dtype=dtype)
     check_moe(y, (x, ids, weights, *w), "silu", False)
+
+
+@pytest.mark.parametrize("M,N,tile", [(5000, 64, None), (5000, 300, None), (4096, 2048, None), (300, 200, "128x128"), (300, 200, "256x192"),
+                                      (300, 200, "256x256"), (300, 200, "256x288")])
+def test_linear_empty_contraction_of_many_rows_and_on_tiles(M, N, tile, monkeypatch):
+    if tile:
+        monkeypatch.setenv("FG_GEMM_TILE", tile)
+    ops = linear_case(1, M, N, 0)
+    bias, residual = rand(1, N), rand(2, M, N)
+    y = torch.full((M, N), float("nan"), device=device())
+    fg.fg_fp8_gemm_fprop_epilogue(*ops, bias=bias, act=fg.FG_ACT_GELU_TANH, residual=residual, y=y)
+    check_linear(ops, y, "gelu", bias, residual)
+
+
+def test_linear_activations_past_32_bits():
+    """A few columns of more than 2^32 bytes of activations: the first, middle and last rows against 64 bits."""
+    M, N, K = 70000, 8, 65536
+    g = torch.Generator(device()).manual_seed(1)
+    xq = torch.randint(0, 0x70, (M, K), dtype=torch.uint8, device=device(), generator=g)
+    wq = torch.randint(0, 0x70, (N, K), dtype=torch.uint8, device=device(), generator=g)
+    sx = torch.rand(K // 128, M, device=device(), generator=g) + 0.5
+    sw = torch.rand(1, K // 128, device=device(), generator=g) + 0.5
+    y = fg.fg_fp8_gemm_fprop_epilogue(xq, sx, wq, sw, out_dtype=torch.float32)
+    for rows in (slice(0, 40), slice(M // 2, M // 2 + 40), slice(M - 40, M)):
+        check_linear((xq[rows], sx[:, rows].contiguous(), wq, sw), y[rows], "none", None, None)

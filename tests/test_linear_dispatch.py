@@ -70,10 +70,24 @@ def test_rows_past_a_grid_go_to_the_tiles(driver):
     assert driver(1, 2, 65535 * 16 + 1, 64, 7168) == (OK, "tiles")
 
 
-def test_no_estimate_beats_the_memory(tmp_path):
-    exe = str(tmp_path / "estimates")
+@pytest.fixture(scope="module")
+def estimates(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("estimates") / "driver")
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc"),
                         os.path.join(ROOT, "tests", "stream_estimate_driver.cpp"), "-o", exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
-    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    return lambda *sizes: subprocess.run([exe, *map(str, sizes)], capture_output=True, text=True, timeout=60)
+
+
+def test_no_estimate_beats_the_memory(estimates):
+    r = estimates()
     assert r.returncode == 0, r.stdout
+
+
+@pytest.mark.parametrize("M,N,K,us", [
+    (8192, 1024, 128, 15.5), (16384, 512, 128, 15.5), (65536, 256, 128, 29.4), (512, 5952, 256, 9.0), (512, 5952, 512, 10.5),
+    (1024, 5952, 512, 17.2), (4096, 2944, 512, 30.1), (16384, 256, 2048, 31.2), (8192, 512, 7168, 85.6),     # 64x32
+    (4096, 8, 16384, 14.3), (8192, 16, 7168, 12.7), (16384, 8, 16384, 48.9)])                                # narrow outputs
+def test_estimates_near_measured_times(estimates, M, N, K, us):
+    """Times of the kernel on an MI355X; boxes and runs differ by up to a tenth, the estimates' steps are as coarse again."""
+    assert 0.8 * us <= float(estimates(M, N, K).stdout) <= 1.25 * us
