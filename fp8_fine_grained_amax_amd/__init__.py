@@ -62,6 +62,7 @@ def lib():
         L.fg_last_hip_error.argtypes = []
         L.fg_last_hip_error.restype = I
         ffn.declare(L)
+        train.declare(L)
         _lib = L
     return _lib
 
@@ -391,3 +392,6 @@ def fg_fp8_grouped_gemm_wgrad(dytq, sdyt, xtq, sxt, offsets, dw=None, accumulate
 from . import ffn  # noqa: E402  (it uses this module's helpers)
 from .ffn import (FG_ACT_GELU_TANH, FG_ACT_NONE, FG_ACT_RELU, FG_ACT_SILU, ActGrad,  # noqa: E402,F401
                   fg_act_checkpoint_bwd, fg_act_checkpoint_fwd, fg_fp8_gemm_fprop_epilogue, fg_moe_few_tokens)
+from . import train  # noqa: E402
+from .train import (FG_NORM_LAYER, FG_NORM_RMS, NormGrad, NormTiles, fg_norm_bwd, fg_norm_quantize,  # noqa: E402,F401
+                    fg_orthogonalize)

@@ -14,8 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8fg.so")
 SOURCES = ["api.hip", "quant.hip", "gemm.hip", "per_tensor.hip", "e5m6.hip", "limited_accum.hip", "act_checkpoint.hip",
-           "stream_linear.hip", "moe_few_tokens.hip"]
-HOST_SOURCES = ["ffn_api.cpp"]          # argument checks only: no device code
+           "stream_linear.hip", "moe_few_tokens.hip", "norm.hip", "ortho.hip"]
+HOST_SOURCES = ["ffn_api.cpp", "train_api.cpp"]          # argument checks only: no device code
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 
@@ -62,7 +62,7 @@ def build(verbose: bool = False, extra=()) -> str:
         # an older binding may not fit the new library; without one, its functions raise at their first call
         if os.path.exists(FFN_MODULE):
             os.remove(FFN_MODULE)
-        sys.stderr.write(f"{os.path.basename(FFN_MODULE)}, the Python binding of the feed-forward operators, is not built: "
+        sys.stderr.write(f"{os.path.basename(FFN_MODULE)}, the Python binding of the feed-forward and training-step operators, is not built: "
                          f"it needs {missing}; the C library is complete\n")
     else:
         build_ffn_module(verbose)
@@ -70,6 +70,7 @@ def build(verbose: bool = False, extra=()) -> str:
 
 
 FFN_MODULE = os.path.join(HERE, "_ffn.so")
+BINDING_SOURCES = ["ffn_binding.cpp", "train_binding.cpp"]
 
 
 def ffn_module_needs() -> str:
@@ -81,7 +82,7 @@ def ffn_module_needs() -> str:
 
 
 def build_ffn_module(verbose: bool = False) -> str:
-    """_ffn.so: the compiled Python binding of the feed-forward operators (csrc/ffn_binding.cpp), against the installed
+    """_ffn.so: the compiled Python binding of the feed-forward and training-step operators (BINDING_SOURCES), against the installed
     torch's headers and libraries and libfp8fg.so in this package directory."""
     import sysconfig
 
@@ -90,14 +91,14 @@ def build_ffn_module(verbose: bool = False) -> str:
     cmd = ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", os.path.join(base, "include"),
            "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"], "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "ffn_binding.cpp"), "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-I", CSRC, *(os.path.join(CSRC, f) for f in BINDING_SOURCES), "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
            "-ltorch_hip", "-lc10", "-lc10_hip", "-L", HERE, "-lfp8fg", "-Wl,-rpath,$ORIGIN", "-o", FFN_MODULE + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stderr + "\n")
-        raise RuntimeError("g++ failed on csrc/ffn_binding.cpp")
+        raise RuntimeError(f"g++ failed on {', '.join(BINDING_SOURCES)} (csrc)")
     r = subprocess.run([sys.executable, "-c", "import ctypes, sys, torch; ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_LOCAL)",
                         FFN_MODULE + ".tmp"], capture_output=True, text=True)
     if r.returncode != 0:

@@ -4,8 +4,8 @@
 // VALU work (three to five quantizations of every element besides the activation), so every tensor is read
 // and written once and the values stay in registers between the maxima and the codes.
 #include "ffn_launch.h"
-#include "ffn_math.h"
 #include "host_util.h"
+#include "tile8.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -27,39 +27,9 @@ hipError_t by_act(int act, Fn&& fn) {
     }
 }
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-        f[2 * p] = fg_bf16_lo(w[p]);
-        f[2 * p + 1] = fg_bf16_hi(w[p]);
-    }
-}
-
 __device__ __forceinline__ uint32_t absmax8_bits(uint4 v) {
     return fg_pk_max_u16(fg_pk_max_u16(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
                          fg_pk_max_u16(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-}
-
-__device__ __forceinline__ float absmax8(const float (&f)[8]) {
-    float m = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; e++) m = __builtin_fmaxf(m, __builtin_fabsf(f[e]));
-    return m;
-}
-
-template <bool SMALL>
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float s) {
-    const fg_divisor d = fg_divisor_of(s);
-    return make_uint2(fg_quant4<SMALL>(f[0], f[1], f[2], f[3], d), fg_quant4<SMALL>(f[4], f[5], f[6], f[7], d));
-}
-
-// Sum over the four lanes l % 16 + 16 i: each row swap leaves the two partners' values in its two results.
-__device__ __forceinline__ float rows_sum(float v) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    const float m = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -144,9 +114,6 @@ __global__ __launch_bounds__(256) void fg_act_fwd_kernel(const uint16_t* __restr
 // a second one for its CU: 256 tiles 14.6 us, 257 19.3, 512 26.5.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 512, kBwdWaves = kBwdThreads / 64;
-
-// 16-byte slot of a column's piece in the transposed image.
-__device__ __forceinline__ int t_slot(int c, int piece) { return ((c ^ ((c >> 6) & 1)) * 8 + (piece ^ ((c >> 3) & 7))); }
 
 // FULL: rows is a multiple of 128. Otherwise no tiling along the rows is asked for, and rows past the end count as
 // zeros of da.

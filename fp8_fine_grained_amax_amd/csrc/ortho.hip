@@ -1,0 +1,392 @@
+// Orthogonalised update by Newton-Schulz products (gfx950): A = X X^T, B = b A + c A A, X = a X + B X, a few times over.
+//
+// Three products a step, m x m x n, m x m x m and m x n x m with m the smaller side, bound by the matrix cores. Operands
+// are fp16: bf16's 8 bits make an update 1e-2 off, fp16's 11 bits 1.3e-3 (simulated, 768 x 2048), at the same rate, and the
+// range suffices, since |X| <= 1 at the start and the steps keep its singular values below about 1.2. X is held times
+// 2^12, whose entries of a large matrix would be denormal otherwise (1e-4), A and B times 2^11 (|B| stays below 30).
+//
+// Every product is one of rows with rows (C[i][j] = sum_k P[i][k] Q[j][k]): X X^T and A A (A is symmetric) as they are, B X
+// from a transposed copy of X that the last product wrote beside X itself. The symmetric ones compute the tiles on and
+// below the diagonal and write each one twice. Contractions are padded with zeros to multiples of 64.
+#include "host_util.h"
+#include "train_launch.h"
+
+#include <algorithm>
+#include <type_traits>
+
+#include "common.h"
+
+namespace {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr int BK = 64;                           // a K step: 128 bytes of a row
+constexpr float kScaleX = 4096.0f, kScaleA = 2048.0f;
+constexpr int kNormParts = 256;                  // partial sums of a matrix's squares, at most
+
+int64_t pad(int64_t v) { return (v + BK - 1) / BK * BK; }
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// C = alpha P Q^T + beta E of every matrix of a batch; E and C have the same shape.
+struct OrthoGemm {
+    const uint16_t *p, *q, *e;                   // fp16 [M][ld], [N][ld], [M][ld_e] or NULL
+    uint16_t *out, *out_t;                       // [M][ld_out], [N][ld_t], either may be NULL: 16 bits an element
+    int64_t p_batch, q_batch, e_batch, out_batch, t_batch;
+    int64_t ld, ld_e, ld_out, ld_t;
+    int M, N, batch;
+    float alpha, beta;
+    int symmetric;                               // out and out_t are the same matrix
+    int bf16;                                    // outputs are bf16 without padding; fp16 with zeros up to their strides if not
+};
+
+__device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base) {
+    const uint64_t u = (uint64_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), (short)0, (int)0xFFFFFFFFu, 0x00020000);
+}
+// Compiled in the device pass only: the host pass does not know the 16-byte form.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* lds, uint32_t voffset) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, FG_LDS(lds), 16, voffset, 0, 0, 0);
+#endif
+}
+
+// Workgroup b runs on XCD b % 8: every XCD gets one contiguous range of tile ids.
+__device__ __forceinline__ int xcd_remap(int b, int total) {
+    const int x = b & 7, base = total >> 3, extra = total & 7;
+    return x * base + (x < extra ? x : extra) + (b >> 3);
+}
+
+// Tile number id of a lower triangle, row by row.
+__device__ __forceinline__ void triangle(int id, int& i, int& j) {
+    i = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
+    while ((i + 1) * (i + 2) / 2 <= id) i++;
+    while (i * (i + 1) / 2 > id) i--;
+    j = id - i * (i + 1) / 2;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+__device__ __forceinline__ uint32_t half_bits(float v, int bf16) {
+    return bf16 ? (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)v) : (uint32_t)__builtin_bit_cast(unsigned short, (_Float16)v);
+}
+
+// ------------------------------------------------------------------------------------------------
+// 128 x 128 x 64 workgroup tiles: 4 waves (2 x 2) of 64 x 64, STAGES K steps in flight (loads go straight to LDS).
+// ------------------------------------------------------------------------------------------------
+struct MidTile {
+    static constexpr int NTHREADS = 256, BM = 128, BN = 128, SUB = 4, STAGE = (BM + BN) * 128, LOADS = 8;
+};
+
+template <int STAGES>
+__global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_kernel(OrthoGemm p) {
+    using C = MidTile;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
+    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
+    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
+    const int64_t batch = id / per;
+    int ti, tj;
+    if (p.symmetric) triangle(local, ti, tj);
+    else ti = local % m_tiles, tj = local / m_tiles;
+    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
+    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+
+    uint32_t a_off[4], b_off[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int row = (wave + 4 * u) * 8 + (lane >> 3);
+        const int rm = m0 + row < p.M ? row : p.M - 1 - m0, rn = n0 + row < p.N ? row : p.N - 1 - n0;    // past the end: the last again
+        const uint32_t chunk = ((lane & 7) ^ swz128(row)) << 4;
+        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + chunk;
+        b_off[u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + chunk;
+    }
+    auto issue = [&](int kb, int slot) {
+        const int k = kb < nkb ? kb : nkb - 1;
+        uint8_t* st = smem + slot * C::STAGE;
+        const auto ra = buffer_rsrc(pp + (int64_t)k * 128), rb = buffer_rsrc(qp + (int64_t)k * 128);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            load_lds16(ra, st + (wave + 4 * u) * 1024, a_off[u]);
+            load_lds16(rb, st + C::BM * 128 + (wave + 4 * u) * 1024, b_off[u]);
+        }
+    };
+    // An operand of 16 rows and 32 of the 64: lane l holds row l % 16 and the 8 values from 8 (l / 16) on.
+    const int lrow = lane & 15, g16 = lane >> 4;
+    const int frag[2] = {lrow * 128 + ((g16 ^ swz128(lrow)) << 4), lrow * 128 + (((4 + g16) ^ swz128(lrow)) << 4)};
+    v8h af[2][C::SUB][2], bf[2][C::SUB][2];
+    auto read = [&](int kb, int set) {
+        const uint8_t* st = smem + (kb & (STAGES - 1)) * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                af[set][i][h] = *reinterpret_cast<const v8h*>(st + (wm * 64 + 16 * i) * 128 + frag[h]);
+                bf[set][i][h] = *reinterpret_cast<const v8h*>(st + C::BM * 128 + (wn * 64 + 16 * i) * 128 + frag[h]);
+            }
+    };
+    v4f acc[C::SUB][C::SUB];
+#pragma unroll
+    for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+    for (int s = 0; s < STAGES; s++) issue(s, s);
+    wait_loads<(STAGES - 1) * C::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(0, 0);
+    // The barrier of step kb says that every wave's part of stage kb + 1 has landed and that stage kb's operands are read,
+    // so its slot takes stage kb + STAGES. Every step issues the same loads (past the end the last block's again, into a slot
+    // that nobody reads).
+    auto step = [&](int kb, auto set_tag) {
+        constexpr int set = decltype(set_tag)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<(STAGES - 2) * C::LOADS>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);             // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        issue(kb + STAGES, kb & (STAGES - 1));
+        read(kb + 1, set ^ 1);
+#pragma unroll
+        for (int t = 0; t < C::SUB * C::SUB; t++) {
+            const int i = t / C::SUB, j = t % C::SUB;
+#pragma unroll
+            for (int h = 0; h < 2; h++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[set][j][h], af[set][i][h], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two MFMAs
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read of the next step's operands
+        }
+    };
+    int kb = 0;
+    for (; kb + 1 < nkb; kb += 2) {
+        step(kb, std::integral_constant<int, 0>{});
+        step(kb + 1, std::integral_constant<int, 1>{});
+    }
+    if (kb < nkb) step(kb, std::integral_constant<int, 0>{});
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();                                    // the stages are free
+
+    // Lane l holds row l % 16 and columns 4 (l / 16) .. + 3 of every 16 x 16 tile. The finished tile goes through an LDS image
+    // [128 rows][16 chunks of 8], chunk c of row r at c ^ (r % 16), and out of it in rows and in columns.
+    const uint16_t* e = p.e ? p.e + batch * p.e_batch : nullptr;
+#pragma unroll
+    for (int i = 0; i < C::SUB; i++) {
+        const int r = wm * 64 + 16 * i + lrow, m = m0 + r;
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) {
+            const int c = wn * 64 + 16 * j + 4 * g16, n = n0 + c;
+            float v[4];
+            uint2 w = make_uint2(0, 0);
+            if (e && m < p.M && n < p.ld_e) w = *reinterpret_cast<const uint2*>(e + (int64_t)m * p.ld_e + n);
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t h = k & 2 ? w.y : w.x;
+                const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
+                v[k] = p.alpha * acc[i][j][k];
+                if (e) v[k] = __builtin_fmaf(p.beta, old, v[k]);
+                if (m >= p.M || n + k >= p.N) v[k] = 0.0f;      // padding
+            }
+            *reinterpret_cast<uint2*>(smem + r * 256 + (((c >> 3) ^ (r & 15)) << 4) + ((c >> 2) & 1) * 8) =
+                make_uint2(half_bits(v[0], p.bf16) | (half_bits(v[1], p.bf16) << 16), half_bits(v[2], p.bf16) | (half_bits(v[3], p.bf16) << 16));
+        }
+    }
+    __syncthreads();
+    // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
+    auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
+        if (p.bf16 && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                if (c + k < width) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        } else if (c < width) {
+            *reinterpret_cast<uint4*>(row + c) = v;
+        }
+    };
+    if (p.out) {
+        uint16_t* out = p.out + batch * p.out_batch;
+        const int width = p.bf16 ? p.N : (int)p.ld_out;
+#pragma unroll
+        for (int it = 0; it < 8; it++) {
+            const int r = it * 16 + (tid >> 4), c = tid & 15;
+            if (m0 + r < p.M)
+                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * 256 + ((c ^ (r & 15)) << 4)));
+        }
+    }
+    if (p.out_t && !(p.symmetric && ti == tj)) {
+        uint16_t* out = p.out_t + batch * p.t_batch;
+        const int width = p.bf16 ? p.M : (int)p.ld_t;
+#pragma unroll
+        for (int it = 0; it < 8; it++) {
+            const int c = (it & 7) * 16 + (tid & 15), r = 8 * (tid >> 4);        // column c, rows r .. r + 7
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const uint32_t h = *reinterpret_cast<const uint16_t*>(smem + (r + k) * 256 + (((c >> 3) ^ ((r + k) & 15)) << 4) + (c & 7) * 2);
+                w[k >> 1] = k & 1 ? w[k >> 1] | (h << 16) : h;
+            }
+            if (n0 + c < p.N) store(out + (int64_t)(n0 + c) * p.ld_t, p.ld_t, m0 + r, width, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The start: |G|, then X and its transpose.
+// ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ float load_g(const FgOrtho& p, int64_t i) {
+    return p.g_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.g)[i] << 16) : ((const float*)p.g)[i];
+}
+
+// Sum over a 256-thread workgroup, in every thread.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// Squares are summed in 64 bits: an fp32 gradient's may leave 32 bits' range either way.
+__global__ __launch_bounds__(256) void fg_ortho_norm_kernel(FgOrtho p, double* __restrict__ partial) {
+    __shared__ double red[4];
+    const int64_t batch = blockIdx.y, segments = (p.K + 1023) / 1024, units = p.N * segments;
+    double s = 0.0;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int64_t row = u / segments, c0 = (u % segments) * 1024 + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (c0 + 256 * k >= p.K) continue;
+            const double v = load_g(p, (batch * p.N + row) * p.ld + c0 + 256 * k);
+            s = __builtin_fma(v, v, s);
+        }
+    }
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) partial[batch * kNormParts + blockIdx.x] = s;
+}
+
+// 64 x 64 elements of G to both copies of X, zeros behind the last row and column.
+__global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const double* __restrict__ partial, int parts, uint16_t* same,
+                                                             uint16_t* turned, int64_t ld_same, int64_t ld_turned) {
+    __shared__ double red[4];
+    __shared__ uint16_t tile[64][66];
+    const int64_t batch = blockIdx.y, tiles = (p.K + 63) / 64;
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles) * 64, c0 = (int64_t)(blockIdx.x % tiles) * 64;
+    const double sum = block_sum((int)threadIdx.x < parts ? partial[batch * kNormParts + threadIdx.x] : 0.0, red);
+    // an fp32 norm that overflows is infinite, and 0 times an infinity NaN
+    const float inv = (float)(1.0 / (double)((float)__builtin_sqrt(sum) + p.eps));
+    const int c = threadIdx.x & 63, rr = threadIdx.x >> 6;
+    same += batch * p.N * ld_same;
+    turned += batch * p.K * ld_turned;
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+        const int r = rr + 4 * k;
+        float v = 0.0f;
+        if (r0 + r < p.N && c0 + c < p.K) v = load_g(p, (batch * p.N + r0 + r) * p.ld + c0 + c) * inv * kScaleX;
+        const uint16_t h = (uint16_t)half_bits(v, 0);
+        tile[r][c] = h;
+        if (r0 + r < p.N) same[(r0 + r) * ld_same + c0 + c] = h;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+        const int r = rr + 4 * k;
+        if (c0 + r < p.K) turned[(c0 + r) * ld_turned + r0 + c] = tile[c][r];
+    }
+}
+
+int64_t mid_tiles(const OrthoGemm& p) {
+    const int64_t m = (p.M + 127) / 128, n = (p.N + 127) / 128;
+    return p.batch * (p.symmetric ? m * (m + 1) / 2 : m * n);
+}
+
+template <int STAGES>
+hipError_t launch_mid(const OrthoGemm& p, hipStream_t stream) {
+    auto kern = fg_ortho_gemm_kernel<STAGES>;
+    static std::atomic<uint64_t> lds_limit_set{0};
+    const hipError_t e = fg_set_lds_limit_once((const void*)kern, STAGES * MidTile::STAGE, lds_limit_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)mid_tiles(p)), dim3(MidTile::NTHREADS), STAGES * MidTile::STAGE, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
+    return mid_tiles(p) <= fg_device_cus() ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
+}
+
+// The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.
+struct Layout {
+    int64_t m, n, mp, np, x, t0, t1, a, b, partial, bytes;
+    Layout(int64_t batch, int64_t N, int64_t K) : m(std::min(N, K)), n(std::max(N, K)), mp(pad(m)), np(pad(n)) {
+        int64_t at = 0;
+        auto take = [&](int64_t size) {
+            const int64_t here = at;
+            at += align256(size);
+            return here;
+        };
+        x = take(2 * batch * m * np);
+        t0 = take(2 * batch * n * mp);
+        t1 = take(2 * batch * n * mp);
+        a = take(2 * batch * m * mp);
+        b = take(2 * batch * m * mp);
+        partial = take(8 * batch * kNormParts);
+        bytes = at;
+    }
+};
+
+}  // namespace
+
+int64_t fg_ortho_workspace_bytes(int64_t batch, int64_t N, int64_t K) { return Layout(batch, N, K).bytes; }
+
+hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
+    const Layout l(o.batch, o.N, o.K);
+    uint8_t* ws = (uint8_t*)o.workspace;
+    uint16_t *x = (uint16_t*)(ws + l.x), *t = (uint16_t*)(ws + l.t0), *t_next = (uint16_t*)(ws + l.t1);
+    uint16_t *a = (uint16_t*)(ws + l.a), *b = (uint16_t*)(ws + l.b);
+    double* partial = (double*)(ws + l.partial);
+    const bool wide = o.N <= o.K;
+    const int parts = (int)std::min<int64_t>(kNormParts, (o.N * ((o.K + 1023) / 1024) + 3) / 4);
+    hipLaunchKernelGGL(fg_ortho_norm_kernel, dim3(parts, (unsigned)o.batch), dim3(256), 0, stream, o, partial);
+    hipLaunchKernelGGL(fg_ortho_start_kernel, dim3((unsigned)(((o.N + 63) / 64) * ((o.K + 63) / 64)), (unsigned)o.batch), dim3(256), 0, stream,
+                       o, partial, parts, wide ? x : t, wide ? t : x, wide ? l.np : l.mp, wide ? l.mp : l.np);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    for (int s = 0; s < o.steps; s++) {
+        OrthoGemm g{};
+        g.batch = (int)o.batch;
+        g.M = g.N = (int)l.m;
+        g.p = g.q = x; g.ld = l.np; g.p_batch = g.q_batch = l.m * l.np;
+        g.out = g.out_t = a; g.ld_out = g.ld_t = l.mp; g.out_batch = g.t_batch = l.m * l.mp;
+        g.alpha = kScaleA / (kScaleX * kScaleX);
+        g.symmetric = 1;
+        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
+        g.p = g.q = g.e = a; g.ld = g.ld_e = l.mp; g.p_batch = g.q_batch = g.e_batch = l.m * l.mp;
+        g.out = g.out_t = b;
+        g.alpha = o.c / kScaleA; g.beta = o.b;
+        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
+        g.p = b; g.q = t; g.q_batch = l.n * l.mp; g.N = (int)l.n;
+        g.e = x; g.ld_e = l.np; g.e_batch = l.m * l.np;
+        g.symmetric = 0;
+        if (s + 1 < o.steps) {
+            g.out = x; g.ld_out = l.np; g.out_batch = l.m * l.np;
+            g.out_t = t_next; g.ld_t = l.mp; g.t_batch = l.n * l.mp;
+            g.alpha = 1.0f / kScaleA; g.beta = o.a;
+        } else {
+            g.out = wide ? o.out : nullptr;
+            g.out_t = wide ? nullptr : o.out;
+            g.ld_out = g.ld_t = o.K; g.out_batch = g.t_batch = o.N * o.K;
+            g.alpha = o.scale / (kScaleA * kScaleX); g.beta = o.a * o.scale / kScaleX;
+            g.bf16 = 1;
+        }
+        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
+        std::swap(t, t_next);
+    }
+    return hipSuccess;
+}
