@@ -68,6 +68,11 @@ __device__ __forceinline__ void triangle(int id, int& i, int& j) {
     j = id - i * (i + 1) / 2;
 }
 
+// Byte of 16-byte chunk c of a row below 16 in a stage. An operand of 16 rows and 32 of the 64 values has row l % 16 and eight of
+// them in lane l: the chunks 2 (l / 16) in one operand and 2 (l / 16) + 1 in the other, for both sides alike. (The order of a
+// contraction is free. With l / 16 and l / 16 + 4 every read had a two-way bank conflict, 5% of the time.)
+__device__ __forceinline__ int frag_at(int row, int c) { return row * 128 + ((c ^ swz128(row)) << 4); }
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
@@ -75,6 +80,91 @@ __device__ __forceinline__ void wait_loads() {
 
 __device__ __forceinline__ uint32_t half_bits(float v, int bf16) {
     return bf16 ? (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)v) : (uint32_t)__builtin_bit_cast(unsigned short, (_Float16)v);
+}
+
+// The end of a workgroup's tile: alpha acc + beta E, stored in rows and, turned, in columns. Lane l holds row l % 16 and columns
+// 4 (l / 16) .. + 3 of every 16 x 16 tile of its wave, whose first row and column in the workgroup's are (wr, wc). The
+// finished tile goes through an LDS image [BM rows][BN / 8 chunks of 8], chunk c of row r at c ^ (r % 16).
+template <int BM, int BN, int THREADS, int MSUB, int NSUB>
+__device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB][NSUB], uint8_t* smem, int64_t batch, int m0, int n0,
+                                       int wr, int wc, bool diagonal) {
+    const int tid = threadIdx.x, lane = tid & 63, lrow = lane & 15, g16 = lane >> 4;
+    uint2 w[MSUB][NSUB];                                        // E's elements, loaded together (in bounds)
+    if (p.e) {
+        const uint16_t* e = p.e + batch * p.e_batch + (int64_t)m0 * p.ld_e;
+#pragma unroll
+        for (int i = 0; i < MSUB; i++) {
+            const int r = wr + 16 * i + lrow;
+            const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld_e;
+#pragma unroll
+            for (int j = 0; j < NSUB; j++) {
+                const int n = n0 + wc + 16 * j + 4 * g16;
+                w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld_e ? n : 0)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < MSUB; i++)
+#pragma unroll
+            for (int j = 0; j < NSUB; j++) w[i][j] = make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < MSUB; i++) {
+        const int r = wr + 16 * i + lrow, m = m0 + r;
+#pragma unroll
+        for (int j = 0; j < NSUB; j++) {
+            const int c = wc + 16 * j + 4 * g16, n = n0 + c;
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t h = k & 2 ? w[i][j].y : w[i][j].x;
+                const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
+                v[k] = __builtin_fmaf(p.beta, old, p.alpha * acc[i][j][k]);
+                if (m >= p.M || n + k >= p.N) v[k] = 0.0f;      // padding
+            }
+            *reinterpret_cast<uint2*>(smem + r * (2 * BN) + (((c >> 3) ^ (r & 15)) << 4) + ((c >> 2) & 1) * 8) =
+                make_uint2(half_bits(v[0], p.bf16) | (half_bits(v[1], p.bf16) << 16), half_bits(v[2], p.bf16) | (half_bits(v[3], p.bf16) << 16));
+        }
+    }
+    __syncthreads();
+    // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
+    auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
+        if (p.bf16 && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                if (c + k < width) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+        } else if (c < width) {
+            *reinterpret_cast<uint4*>(row + c) = v;
+        }
+    };
+    if (p.out) {
+        constexpr int CH = BN / 8;
+        uint16_t* out = p.out + batch * p.out_batch;
+        const int width = p.bf16 ? p.N : (int)p.ld_out;
+#pragma unroll 4
+        for (int f = tid; f < BM * CH; f += THREADS) {
+            const int r = f / CH, c = f % CH;
+            if (m0 + r < p.M)
+                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & 15)) << 4)));
+        }
+    }
+    if (p.out_t && !diagonal) {
+        constexpr int CH = BM / 8;
+        uint16_t* out = p.out_t + batch * p.t_batch;
+        const int width = p.bf16 ? p.M : (int)p.ld_t;
+#pragma unroll 2
+        for (int f = tid; f < BN * CH; f += THREADS) {
+            const int c = f % 16 + f / (16 * CH) * 16, r = 8 * (f / 16 % CH);        // column c, rows r .. r + 7
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const uint32_t h = *reinterpret_cast<const uint16_t*>(smem + (r + k) * (2 * BN) + (((c >> 3) ^ ((r + k) & 15)) << 4) + (c & 7) * 2);
+                w[k >> 1] = k & 1 ? w[k >> 1] | (h << 16) : h;
+            }
+            if (n0 + c < p.N) store(out + (int64_t)(n0 + c) * p.ld_t, p.ld_t, m0 + r, width, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -120,9 +210,8 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_k
             load_lds16(rb, st + C::BM * 128 + (wave + 4 * u) * 1024, b_off[u]);
         }
     };
-    // An operand of 16 rows and 32 of the 64: lane l holds row l % 16 and the 8 values from 8 (l / 16) on.
     const int lrow = lane & 15, g16 = lane >> 4;
-    const int frag[2] = {lrow * 128 + ((g16 ^ swz128(lrow)) << 4), lrow * 128 + (((4 + g16) ^ swz128(lrow)) << 4)};
+    const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
     v8h af[2][C::SUB][2], bf[2][C::SUB][2];
     auto read = [&](int kb, int set) {
         const uint8_t* st = smem + (kb & (STAGES - 1)) * C::STAGE;
@@ -176,67 +265,139 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_k
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();                                    // the stages are free
 
-    // Lane l holds row l % 16 and columns 4 (l / 16) .. + 3 of every 16 x 16 tile. The finished tile goes through an LDS image
-    // [128 rows][16 chunks of 8], chunk c of row r at c ^ (r % 16), and out of it in rows and in columns.
-    const uint16_t* e = p.e ? p.e + batch * p.e_batch : nullptr;
-#pragma unroll
-    for (int i = 0; i < C::SUB; i++) {
-        const int r = wm * 64 + 16 * i + lrow, m = m0 + r;
-#pragma unroll
-        for (int j = 0; j < C::SUB; j++) {
-            const int c = wn * 64 + 16 * j + 4 * g16, n = n0 + c;
-            float v[4];
-            uint2 w = make_uint2(0, 0);
-            if (e && m < p.M && n < p.ld_e) w = *reinterpret_cast<const uint2*>(e + (int64_t)m * p.ld_e + n);
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const uint32_t h = k & 2 ? w.y : w.x;
-                const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
-                v[k] = p.alpha * acc[i][j][k];
-                if (e) v[k] = __builtin_fmaf(p.beta, old, v[k]);
-                if (m >= p.M || n + k >= p.N) v[k] = 0.0f;      // padding
-            }
-            *reinterpret_cast<uint2*>(smem + r * 256 + (((c >> 3) ^ (r & 15)) << 4) + ((c >> 2) & 1) * 8) =
-                make_uint2(half_bits(v[0], p.bf16) | (half_bits(v[1], p.bf16) << 16), half_bits(v[2], p.bf16) | (half_bits(v[3], p.bf16) << 16));
-        }
+    finish<C::BM, C::BN, C::NTHREADS>(p, acc, smem, batch, m0, n0, wm * 64, wn * 64, p.symmetric && ti == tj);
+}
+
+// ------------------------------------------------------------------------------------------------
+// 256 x 256 x 64 workgroup tiles: 8 waves (2 x 4) of 128 x 64, two on a SIMD, which take turns: while one issues 16 MFMAs (a
+// quarter of its tile's K step, 64 x 32), the other reads its next operands from LDS and issues loads. Two barriers a
+// quarter keep them apart; the waves of the second group are one barrier behind.
+//
+// The quarters go (A0, B0), (A0, B1), (A1, B1), (A1, B0), so each half of a wave's operands is read once a step. Two stages of
+// 64 KB: a half that both groups have read is loaded over at once with the step after next's, so that a load has seven of a
+// step's eight turns to land. What a quarter reads is waited for in the turn before, in front of a barrier; loads return in
+// order, so the counts of those that may be outstanding are fixed: a wave's loads are A0 and B0 (4) in quarter 1, B1 (2) in
+// quarter 2, A1 (2) in quarter 3.
+// ------------------------------------------------------------------------------------------------
+struct BigTile {
+    static constexpr int NTHREADS = 512, BM = 256, BN = 256, MSUB = 8, NSUB = 4, STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
+};
+
+__global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(OrthoGemm p) {
+    using C = BigTile;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
+    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
+    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
+    const int64_t batch = id / per;
+    int ti, tj;
+    if (p.symmetric) {
+        triangle(local, ti, tj);
+    } else {
+        constexpr int GM = 8;                            // rows of tiles that an XCD's run goes down together
+        const int group = local / (GM * n_tiles), first = group * GM, rows = min(m_tiles - first, GM), within = local - group * GM * n_tiles;
+        ti = first + within % rows;
+        tj = within / rows;
     }
-    __syncthreads();
-    // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
-    auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
-        if (p.bf16 && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
+    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+
+    // Loads: an instruction fills 8 rows of 128 bytes. A0 is rows [0, 64) and [128, 192) of the tile, B0 the first 32 of every 64
+    // columns; a wave loads 16 rows of each half.
+    auto a_row = [&](int half, int u) { return (wave >> 2) * 128 + half * 64 + (wave & 3) * 16 + u * 8; };
+    auto b_row = [&](int half, int u) { return (wave >> 1) * 64 + half * 32 + (wave & 1) * 16 + u * 8; };
+    uint32_t a_off[2][2], b_off[2][2];
 #pragma unroll
-            for (int k = 0; k < 8; k++)
-                if (c + k < width) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-        } else if (c < width) {
-            *reinterpret_cast<uint4*>(row + c) = v;
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const int ra = a_row(h, u) + (lane >> 3), rb = b_row(h, u) + (lane >> 3);
+            const int rm = m0 + ra < p.M ? ra : p.M - 1 - m0, rn = n0 + rb < p.N ? rb : p.N - 1 - n0;    // past the end: the last again
+            a_off[h][u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(ra)) << 4);
+            b_off[h][u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(rb)) << 4);
         }
+    auto load_a = [&](int kb, int half) {
+        const auto rs = buffer_rsrc(pp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
+#pragma unroll
+        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + a_row(half, u) * 128, a_off[half][u]);
     };
-    if (p.out) {
-        uint16_t* out = p.out + batch * p.out_batch;
-        const int width = p.bf16 ? p.N : (int)p.ld_out;
+    auto load_b = [&](int kb, int half) {
+        const auto rs = buffer_rsrc(qp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
 #pragma unroll
-        for (int it = 0; it < 8; it++) {
-            const int r = it * 16 + (tid >> 4), c = tid & 15;
-            if (m0 + r < p.M)
-                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * 256 + ((c ^ (r & 15)) << 4)));
-        }
+        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + (C::BM + b_row(half, u)) * 128, b_off[half][u]);
+    };
+
+    const int lrow = lane & 15, g16 = lane >> 4;
+    const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
+    v8h af[4][2], bf[C::NSUB][2];                        // a half of A's 16-row operands, and B's
+    auto read_a = [&](int kb, int half) {
+        const uint8_t* st = smem + (kb & 1) * C::STAGE + (wm * 128 + half * 64) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) af[i][h] = *reinterpret_cast<const v8h*>(st + 16 * i * 128 + frag[h]);
+    };
+    auto read_b = [&](int kb) {
+        const uint8_t* st = smem + (kb & 1) * C::STAGE + (C::BM + wn * 64) * 128;
+#pragma unroll
+        for (int j = 0; j < C::NSUB; j++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) bf[j][h] = *reinterpret_cast<const v8h*>(st + 16 * j * 128 + frag[h]);
+    };
+    v4f acc[C::MSUB][C::NSUB];
+#pragma unroll
+    for (int i = 0; i < C::MSUB; i++)
+#pragma unroll
+        for (int j = 0; j < C::NSUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    // The turn of the matrix cores: the operands are there (lgkmcnt), and so is what the next turn reads, on every wave.
+    auto multiply = [&](int half) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < C::NSUB; j++)
+                    acc[4 * half + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][h], af[i][h], acc[4 * half + i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_first = [&](int kb) {
+        load_a(kb, 0);
+        load_b(kb, 0);
+        load_b(kb, 1);
+    };
+    load_first(0);
+    load_a(0, 1);
+    load_first(1);
+    wait_loads<8>();
+    __builtin_amdgcn_s_barrier();
+    if (wm == 1) __builtin_amdgcn_s_barrier();           // the second group
+    __builtin_amdgcn_sched_barrier(0);
+    for (int kb = 0; kb < nkb; kb++) {
+        read_b(kb);
+        read_a(kb, 0);
+        load_a(kb + 1, 1);
+        wait_loads<8>();                                 // A1 of this step
+        multiply(0);
+        read_a(kb, 1);
+        load_first(kb + 2);
+        wait_loads<8>();                                 // A0 and B of the next step
+        multiply(1);
     }
-    if (p.out_t && !(p.symmetric && ti == tj)) {
-        uint16_t* out = p.out_t + batch * p.t_batch;
-        const int width = p.bf16 ? p.M : (int)p.ld_t;
-#pragma unroll
-        for (int it = 0; it < 8; it++) {
-            const int c = (it & 7) * 16 + (tid & 15), r = 8 * (tid >> 4);        // column c, rows r .. r + 7
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const uint32_t h = *reinterpret_cast<const uint16_t*>(smem + (r + k) * 256 + (((c >> 3) ^ ((r + k) & 15)) << 4) + (c & 7) * 2);
-                w[k >> 1] = k & 1 ? w[k >> 1] | (h << 16) : h;
-            }
-            if (n0 + c < p.N) store(out + (int64_t)(n0 + c) * p.ld_t, p.ld_t, m0 + r, width, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-    }
+    if (wm == 0) __builtin_amdgcn_s_barrier();           // every wave passes the same number of barriers
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();                                     // the stages are free
+    finish<C::BM, C::BN, C::NTHREADS>(p, acc, smem, batch, m0, n0, wm * 128, wn * 64, p.symmetric && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -303,23 +464,31 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
     }
 }
 
-int64_t mid_tiles(const OrthoGemm& p) {
-    const int64_t m = (p.M + 127) / 128, n = (p.N + 127) / 128;
+int64_t tiles_of(const OrthoGemm& p, int side) {
+    const int64_t m = (p.M + side - 1) / side, n = (p.N + side - 1) / side;
     return p.batch * (p.symmetric ? m * (m + 1) / 2 : m * n);
+}
+
+template <class Kernel>
+hipError_t launch(Kernel kern, std::atomic<uint64_t>& limit_set, int64_t tiles, int threads, int lds, const OrthoGemm& p, hipStream_t stream) {
+    const hipError_t e = fg_set_lds_limit_once((const void*)kern, lds, limit_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(threads), lds, stream, p);
+    return hipGetLastError();
 }
 
 template <int STAGES>
 hipError_t launch_mid(const OrthoGemm& p, hipStream_t stream) {
-    auto kern = fg_ortho_gemm_kernel<STAGES>;
-    static std::atomic<uint64_t> lds_limit_set{0};
-    const hipError_t e = fg_set_lds_limit_once((const void*)kern, STAGES * MidTile::STAGE, lds_limit_set);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)mid_tiles(p)), dim3(MidTile::NTHREADS), STAGES * MidTile::STAGE, stream, p);
-    return hipGetLastError();
+    static std::atomic<uint64_t> limit_set{0};
+    return launch(fg_ortho_gemm_kernel<STAGES>, limit_set, tiles_of(p, 128), MidTile::NTHREADS, STAGES * MidTile::STAGE, p, stream);
 }
 
 hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
-    return mid_tiles(p) <= fg_device_cus() ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
+    static std::atomic<uint64_t> limit_set{0};
+    const int64_t cus = fg_device_cus(), mid = tiles_of(p, 128), big = tiles_of(p, 256);
+    if ((big + cus - 1) / cus * 2.6 < (mid + 2 * cus - 1) / (2 * cus) * 2.0)
+        return launch(fg_ortho_big_kernel, limit_set, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
+    return mid <= cus ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
 }
 
 // The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.
