@@ -54,6 +54,11 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* lds,
 #endif
 }
 
+typedef short v4s __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v2i tr_read(const uint8_t* lds) {
+    return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)lds));
+}
+
 // Workgroup b runs on XCD b % 8: every XCD gets one contiguous range of tile ids.
 __device__ __forceinline__ int xcd_remap(int b, int total) {
     const int x = b & 7, base = total >> 3, extra = total & 7;
@@ -82,23 +87,20 @@ __device__ __forceinline__ uint32_t half_bits(float v, int bf16) {
     return bf16 ? (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)v) : (uint32_t)__builtin_bit_cast(unsigned short, (_Float16)v);
 }
 
-// The end of a workgroup's tile: alpha acc + beta E, stored in rows and, turned, in columns. Lane l holds row l % 16 and columns
-// 4 (l / 16) .. + 3 of every 16 x 16 tile of its wave, whose first row and column in the workgroup's are (wr, wc). The
-// finished tile goes through an LDS image [BM rows][BN / 8 chunks of 8], chunk c of row r at c ^ (r % 16).
-template <int BM, int BN, int THREADS, int MSUB, int NSUB>
-__device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB][NSUB], uint8_t* smem, int64_t batch, int m0, int n0,
-                                       int wr, int wc, bool diagonal) {
-    const int tid = threadIdx.x, lane = tid & 63, lrow = lane & 15, g16 = lane >> 4;
-    uint2 w[MSUB][NSUB];                                        // E's elements, loaded together (in bounds)
+// E's elements of a wave's 16 x 16 tiles, four to a lane, loaded together (in bounds); zeros without E. (wr, wc): the wave's first
+// row and column in the workgroup's tile.
+template <int MSUB, int NSUB>
+__device__ __forceinline__ void load_e(const OrthoGemm& p, uint2 (&w)[MSUB][NSUB], int64_t batch, int m0, int n0, int wr, int wc) {
     if (p.e) {
+        const int lane = threadIdx.x & 63;
         const uint16_t* e = p.e + batch * p.e_batch + (int64_t)m0 * p.ld_e;
 #pragma unroll
         for (int i = 0; i < MSUB; i++) {
-            const int r = wr + 16 * i + lrow;
+            const int r = wr + 16 * i + (lane & 15);
             const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld_e;
 #pragma unroll
             for (int j = 0; j < NSUB; j++) {
-                const int n = n0 + wc + 16 * j + 4 * g16;
+                const int n = n0 + wc + 16 * j + 4 * (lane >> 4);
                 w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld_e ? n : 0)));
             }
         }
@@ -108,6 +110,17 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
 #pragma unroll
             for (int j = 0; j < NSUB; j++) w[i][j] = make_uint2(0, 0);
     }
+}
+
+// The end of a workgroup's tile: alpha acc + beta E, stored in rows and, turned, in columns. Lane l holds row l % 16 and columns
+// 4 (l / 16) .. + 3 of every 16 x 16 tile. The finished tile goes through an LDS image [BM rows][BN / 8 chunks of 8], chunk c
+// of row r at c ^ (r % 16) (% 8 with 64 columns), which is read in rows, and in columns by the transposing read: 16 lanes
+// read 4 rows x 16 columns, four columns a lane, and each gets one column's four rows.
+template <int BM, int BN, int THREADS, int MSUB, int NSUB>
+__device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB][NSUB], const uint2 (&w)[MSUB][NSUB], uint8_t* smem,
+                                       int64_t batch, int m0, int n0, int wr, int wc, bool diagonal) {
+    constexpr int MIX = BN / 8 < 16 ? BN / 8 - 1 : 15;
+    const int tid = threadIdx.x, lane = tid & 63, lrow = lane & 15, g16 = lane >> 4;
 #pragma unroll
     for (int i = 0; i < MSUB; i++) {
         const int r = wr + 16 * i + lrow, m = m0 + r;
@@ -122,7 +135,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
                 v[k] = __builtin_fmaf(p.beta, old, p.alpha * acc[i][j][k]);
                 if (m >= p.M || n + k >= p.N) v[k] = 0.0f;      // padding
             }
-            *reinterpret_cast<uint2*>(smem + r * (2 * BN) + (((c >> 3) ^ (r & 15)) << 4) + ((c >> 2) & 1) * 8) =
+            *reinterpret_cast<uint2*>(smem + r * (2 * BN) + (((c >> 3) ^ (r & MIX)) << 4) + ((c >> 2) & 1) * 8) =
                 make_uint2(half_bits(v[0], p.bf16) | (half_bits(v[1], p.bf16) << 16), half_bits(v[2], p.bf16) | (half_bits(v[3], p.bf16) << 16));
         }
     }
@@ -130,10 +143,10 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
     // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
     auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
         if (p.bf16 && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 8; k++)
-                if (c + k < width) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+                if (c + k < width) row[c + k] = (uint16_t)(h[k >> 1] >> (16 * (k & 1)));
         } else if (c < width) {
             *reinterpret_cast<uint4*>(row + c) = v;
         }
@@ -146,7 +159,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
         for (int f = tid; f < BM * CH; f += THREADS) {
             const int r = f / CH, c = f % CH;
             if (m0 + r < p.M)
-                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & 15)) << 4)));
+                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & MIX)) << 4)));
         }
     }
     if (p.out_t && !diagonal) {
@@ -155,14 +168,15 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
         const int width = p.bf16 ? p.M : (int)p.ld_t;
 #pragma unroll 2
         for (int f = tid; f < BN * CH; f += THREADS) {
-            const int c = f % 16 + f / (16 * CH) * 16, r = 8 * (f / 16 % CH);        // column c, rows r .. r + 7
-            uint32_t w[4];
+            const int c0 = f / (16 * CH) * 16, r = 8 * (f / 16 % CH), col = c0 + 4 * (lrow & 3);     // column c0 + lrow, rows r .. r + 7
+            v2i part[2];
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const uint32_t h = *reinterpret_cast<const uint16_t*>(smem + (r + k) * (2 * BN) + (((c >> 3) ^ ((r + k) & 15)) << 4) + (c & 7) * 2);
-                w[k >> 1] = k & 1 ? w[k >> 1] | (h << 16) : h;
+            for (int h = 0; h < 2; h++) {
+                const int row = r + 4 * h + (lrow >> 2);
+                part[h] = tr_read(smem + row * (2 * BN) + (((col >> 3) ^ (row & MIX)) << 4) + ((col >> 2) & 1) * 8);
             }
-            if (n0 + c < p.N) store(out + (int64_t)(n0 + c) * p.ld_t, p.ld_t, m0 + r, width, make_uint4(w[0], w[1], w[2], w[3]));
+            const int n = n0 + c0 + lrow;
+            if (n < p.N) store(out + (int64_t)n * p.ld_t, p.ld_t, m0 + r, width, make_uint4(part[0].x, part[0].y, part[1].x, part[1].y));
         }
     }
 }
@@ -229,6 +243,9 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_k
 #pragma unroll
         for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
+    uint2 e[C::SUB][C::SUB];
+    load_e(p, e, batch, m0, n0, wm * 64, wn * 64);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < STAGES; s++) issue(s, s);
     wait_loads<(STAGES - 1) * C::LOADS>();
@@ -265,7 +282,7 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_k
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();                                    // the stages are free
 
-    finish<C::BM, C::BN, C::NTHREADS>(p, acc, smem, batch, m0, n0, wm * 64, wn * 64, p.symmetric && ti == tj);
+    finish<C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 64, wn * 64, p.symmetric && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -397,70 +414,211 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     if (wm == 0) __builtin_amdgcn_s_barrier();           // every wave passes the same number of barriers
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();                                     // the stages are free
-    finish<C::BM, C::BN, C::NTHREADS>(p, acc, smem, batch, m0, n0, wm * 128, wn * 64, p.symmetric && ti == tj);
+    uint2 e[C::MSUB][C::NSUB];
+    load_e(p, e, batch, m0, n0, wm * 128, wn * 64);
+    finish<C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 128, wn * 64, p.symmetric && ti == tj);
+}
+
+// ------------------------------------------------------------------------------------------------
+// 64 x 64 workgroup tiles for small matrices: 4 waves, each with a quarter of the contraction (every fourth K step) for the whole
+// tile and a ring of two stages of its own, so that nothing waits for another wave before the sums are joined, in LDS and in
+// the order of the waves.
+// ------------------------------------------------------------------------------------------------
+struct SmallTile {
+    static constexpr int NTHREADS = 256, WAVES = 4, SIDE = 64, SUB = 4, STAGE = 2 * SIDE * 128, LOADS = 16, LDS = WAVES * 2 * STAGE;
+};
+
+__global__ __launch_bounds__(SmallTile::NTHREADS, 1) void fg_ortho_small_kernel(OrthoGemm p) {
+    using C = SmallTile;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m_tiles = (p.M + C::SIDE - 1) / C::SIDE, n_tiles = (p.N + C::SIDE - 1) / C::SIDE;
+    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
+    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
+    const int64_t batch = id / per;
+    int ti, tj;
+    if (p.symmetric) triangle(local, ti, tj);
+    else ti = local % m_tiles, tj = local / m_tiles;
+    const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = (int)(p.ld / BK);
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
+    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+    uint8_t* ring = smem + wave * (2 * C::STAGE);
+
+    uint32_t a_off[8], b_off[8];
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+        const int row = u * 8 + (lane >> 3);
+        const int rm = m0 + row < p.M ? row : p.M - 1 - m0, rn = n0 + row < p.N ? row : p.N - 1 - n0;    // past the end: the last again
+        const uint32_t chunk = ((lane & 7) ^ swz128(row)) << 4;
+        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + chunk;
+        b_off[u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + chunk;
+    }
+    auto issue = [&](int kb, int slot) {                 // past the end: the last again, into a slot that nobody reads
+        const int k = kb < nkb ? kb : nkb - 1;
+        const auto ra = buffer_rsrc(pp + (int64_t)k * 128), rb = buffer_rsrc(qp + (int64_t)k * 128);
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            load_lds16(ra, ring + slot * C::STAGE + u * 1024, a_off[u]);
+            load_lds16(rb, ring + slot * C::STAGE + C::SIDE * 128 + u * 1024, b_off[u]);
+        }
+    };
+    const int lrow = lane & 15, g16 = lane >> 4;
+    const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
+    v4f acc[C::SUB][C::SUB];
+#pragma unroll
+    for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    uint2 e[1][C::SUB];                                  // of the strip of 16 rows that the wave ends with
+    load_e(p, e, batch, m0, n0, 16 * wave, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue(wave, 0);
+    issue(wave + C::WAVES, 1);
+    int slot = 0;
+    for (int kb = wave; kb < nkb; kb += C::WAVES, slot ^= 1) {
+        wait_loads<C::LOADS>();                          // this step's, with the next one's outstanding
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* st = ring + slot * C::STAGE;
+        v8h af[C::SUB][2], bf[C::SUB][2];
+#pragma unroll
+        for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                af[i][h] = *reinterpret_cast<const v8h*>(st + 16 * i * 128 + frag[h]);
+                bf[i][h] = *reinterpret_cast<const v8h*>(st + C::SIDE * 128 + 16 * i * 128 + frag[h]);
+            }
+        __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the slot is read
+        __builtin_amdgcn_sched_barrier(0);
+        issue(kb + 2 * C::WAVES, slot);
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+                for (int j = 0; j < C::SUB; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[j][h], af[i][h], acc[i][j], 0, 0, 0);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();                                     // the rings are free
+    v4f* red = reinterpret_cast<v4f*>(smem);             // [wave][strip][column tile][lane]
+#pragma unroll
+    for (int i = 0; i < C::SUB; i++)
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) red[((wave * C::SUB + i) * C::SUB + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    v4f sum[1][C::SUB];
+#pragma unroll
+    for (int j = 0; j < C::SUB; j++) {
+        sum[0][j] = red[(wave * C::SUB + j) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < C::WAVES; w++) sum[0][j] += red[((w * C::SUB + wave) * C::SUB + j) * 64 + lane];
+    }
+    finish<C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, p.symmetric && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
 // The start: |G|, then X and its transpose.
 // ------------------------------------------------------------------------------------------------
-__device__ __forceinline__ float load_g(const FgOrtho& p, int64_t i) {
-    return p.g_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.g)[i] << 16) : ((const float*)p.g)[i];
+// Four neighbouring elements of G from element i on, the first `count` of them; `whole`: all four, aligned to their size.
+__device__ __forceinline__ v4f load_g(const FgOrtho& p, int64_t i, int64_t count, bool whole) {
+    v4f v = {0.f, 0.f, 0.f, 0.f};
+    if (whole) {
+        if (!p.g_bf16) return *reinterpret_cast<const v4f*>((const float*)p.g + i);
+        const uint2 w = *reinterpret_cast<const uint2*>((const uint16_t*)p.g + i);
+        return v4f{fg_bf16_lo(w.x), fg_bf16_hi(w.x), fg_bf16_lo(w.y), fg_bf16_hi(w.y)};
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (k < count) v[k] = p.g_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p.g)[i + k] << 16) : ((const float*)p.g)[i + k];
+    return v;
 }
+// Whether every four elements from a multiple of four columns on may be loaded at once (but those that the row's end cuts).
+__device__ __forceinline__ bool fours_aligned(const FgOrtho& p) { return p.ld % 4 == 0 && ((uintptr_t)p.g & (p.g_bf16 ? 7 : 15)) == 0; }
 
-// Sum over a 256-thread workgroup, in every thread.
+// Sum over a workgroup of WAVES waves, in every thread.
+template <int WAVES>
 __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
     for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
-// Squares are summed in 64 bits: an fp32 gradient's may leave 32 bits' range either way.
-__global__ __launch_bounds__(256) void fg_ortho_norm_kernel(FgOrtho p, double* __restrict__ partial) {
-    __shared__ double red[4];
-    const int64_t batch = blockIdx.y, segments = (p.K + 1023) / 1024, units = p.N * segments;
     double s = 0.0;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t row = u / segments, c0 = (u % segments) * 1024 + threadIdx.x;
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            if (c0 + 256 * k >= p.K) continue;
-            const double v = load_g(p, (batch * p.N + row) * p.ld + c0 + 256 * k);
-            s = __builtin_fma(v, v, s);
-        }
-    }
-    s = block_sum(s, red);
-    if (threadIdx.x == 0) partial[batch * kNormParts + blockIdx.x] = s;
+    for (int w = 0; w < WAVES; w++) s += red[w];
+    return s;
 }
 
-// 64 x 64 elements of G to both copies of X, zeros behind the last row and column.
+// Squares are summed in 64 bits: an fp32 gradient's may leave 32 bits' range either way. Bound by HBM: 512 threads a workgroup,
+// four loads of four elements in flight each.
+constexpr int kNormThreads = 512;
+__global__ __launch_bounds__(kNormThreads) void fg_ortho_norm_kernel(FgOrtho p, double* __restrict__ partial) {
+    __shared__ double red[kNormThreads / 64];
+    const int64_t batch = blockIdx.y, fours = (p.K + 3) / 4, total = p.N * fours, step = (int64_t)gridDim.x * kNormThreads;
+    const int64_t row_step = step / fours, col_step = step % fours;
+    const bool aligned = fours_aligned(p);
+    int64_t at = (int64_t)blockIdx.x * kNormThreads + threadIdx.x, row = at / fours, col = at % fours;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    while (at < total) {
+        v4f v[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            v[u] = v4f{0.f, 0.f, 0.f, 0.f};
+            if (at < total) v[u] = load_g(p, (batch * p.N + row) * p.ld + 4 * col, p.K - 4 * col, aligned && 4 * col + 4 <= p.K);
+            at += step;
+            row += row_step;
+            col += col_step;
+            if (col >= fours) {
+                col -= fours;
+                row++;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) s[k] = __builtin_fma((double)v[u][k], (double)v[u][k], s[k]);
+    }
+    const double sum = block_sum<kNormThreads / 64>((s[0] + s[1]) + (s[2] + s[3]), red);
+    if (threadIdx.x == 0) partial[batch * kNormParts + blockIdx.x] = sum;
+}
+
+// 64 x 64 elements of G to both copies of X, zeros behind the last row and column. A thread takes 4 x 4 of them.
 __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const double* __restrict__ partial, int parts, uint16_t* same,
                                                              uint16_t* turned, int64_t ld_same, int64_t ld_turned) {
     __shared__ double red[4];
-    __shared__ uint16_t tile[64][66];
+    __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];       // [column][row]
     const int64_t batch = blockIdx.y, tiles = (p.K + 63) / 64;
     const int64_t r0 = (int64_t)(blockIdx.x / tiles) * 64, c0 = (int64_t)(blockIdx.x % tiles) * 64;
-    const double sum = block_sum((int)threadIdx.x < parts ? partial[batch * kNormParts + threadIdx.x] : 0.0, red);
-    // an fp32 norm that overflows is infinite, and 0 times an infinity NaN
-    const float inv = (float)(1.0 / (double)((float)__builtin_sqrt(sum) + p.eps));
-    const int c = threadIdx.x & 63, rr = threadIdx.x >> 6;
+    const int c = 4 * (threadIdx.x & 15), r = 4 * (threadIdx.x >> 4);
+    const bool whole = fours_aligned(p) && c0 + c + 4 <= p.K;
+    v4f v[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        v[k] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (r0 + r + k < p.N) v[k] = load_g(p, (batch * p.N + r0 + r + k) * p.ld + c0 + c, p.K - c0 - c, whole && c0 + c < p.K);
+    }
+    const double sum = block_sum<4>((int)threadIdx.x < parts ? partial[batch * kNormParts + threadIdx.x] : 0.0, red);
+    const float norm = (float)__builtin_sqrt(sum);
+    const float inv = norm < __builtin_inff() ? (float)(1.0 / (double)(norm + p.eps)) : __builtin_nanf("");
     same += batch * p.N * ld_same;
     turned += batch * p.K * ld_turned;
+    uint32_t h[4][4];
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-        const int r = rr + 4 * k;
-        float v = 0.0f;
-        if (r0 + r < p.N && c0 + c < p.K) v = load_g(p, (batch * p.N + r0 + r) * p.ld + c0 + c) * inv * kScaleX;
-        const uint16_t h = (uint16_t)half_bits(v, 0);
-        tile[r][c] = h;
-        if (r0 + r < p.N) same[(r0 + r) * ld_same + c0 + c] = h;
+    for (int k = 0; k < 4; k++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const bool there = r0 + r + k < p.N && c0 + c + j < p.K;     // a factor of NaN leaves the padding 0
+            h[k][j] = there ? half_bits(v[k][j] * inv * kScaleX, 0) : 0;
+        }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        if (r0 + r + k < p.N)
+            *reinterpret_cast<uint2*>(same + (r0 + r + k) * ld_same + c0 + c) = make_uint2(h[k][0] | (h[k][1] << 16), h[k][2] | (h[k][3] << 16));
+        *reinterpret_cast<uint2*>(&tile[c + k][r]) = make_uint2(h[0][k] | (h[1][k] << 16), h[2][k] | (h[3][k] << 16));
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-        const int r = rr + 4 * k;
-        if (c0 + r < p.K) turned[(c0 + r) * ld_turned + r0 + c] = tile[c][r];
+    for (int k = 0; k < 4; k++) {
+        const int col = (threadIdx.x >> 4) + 16 * k, row = 4 * (threadIdx.x & 15);
+        if (c0 + col < p.K) *reinterpret_cast<uint2*>(turned + (c0 + col) * ld_turned + r0 + row) = *reinterpret_cast<const uint2*>(&tile[col][row]);
     }
 }
 
@@ -484,10 +642,18 @@ hipError_t launch_mid(const OrthoGemm& p, hipStream_t stream) {
 }
 
 hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
-    static std::atomic<uint64_t> limit_set{0};
-    const int64_t cus = fg_device_cus(), mid = tiles_of(p, 128), big = tiles_of(p, 256);
+    static std::atomic<uint64_t> limit_big{0}, limit_small{0};
+    const int64_t cus = fg_device_cus(), mid = tiles_of(p, 128), big = tiles_of(p, 256), small = tiles_of(p, 64);
+#ifdef FORCE
+    const char* f = getenv("FG_F");
+    if (f && *f == 's') return launch(fg_ortho_small_kernel, limit_small, small, SmallTile::NTHREADS, SmallTile::LDS, p, stream);
+    if (f && *f == 'b') return launch(fg_ortho_big_kernel, limit_big, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
+    if (f && *f == '4') return launch_mid<4>(p, stream);
+    if (f && *f == '2') return launch_mid<2>(p, stream);
+#endif
     if ((big + cus - 1) / cus * 2.6 < (mid + 2 * cus - 1) / (2 * cus) * 2.0)
-        return launch(fg_ortho_big_kernel, limit_set, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
+        return launch(fg_ortho_big_kernel, limit_big, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
+    if (small <= 2 * cus) return launch(fg_ortho_small_kernel, limit_small, small, SmallTile::NTHREADS, SmallTile::LDS, p, stream);
     return mid <= cus ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
 }
 
@@ -522,8 +688,8 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
     uint16_t *a = (uint16_t*)(ws + l.a), *b = (uint16_t*)(ws + l.b);
     double* partial = (double*)(ws + l.partial);
     const bool wide = o.N <= o.K;
-    const int parts = (int)std::min<int64_t>(kNormParts, (o.N * ((o.K + 1023) / 1024) + 3) / 4);
-    hipLaunchKernelGGL(fg_ortho_norm_kernel, dim3(parts, (unsigned)o.batch), dim3(256), 0, stream, o, partial);
+    const int parts = (int)std::min<int64_t>(kNormParts, (o.N * ((o.K + 3) / 4) + 2 * kNormThreads - 1) / (2 * kNormThreads));
+    hipLaunchKernelGGL(fg_ortho_norm_kernel, dim3(parts, (unsigned)o.batch), dim3(kNormThreads), 0, stream, o, partial);
     hipLaunchKernelGGL(fg_ortho_start_kernel, dim3((unsigned)(((o.N + 63) / 64) * ((o.K + 63) / 64)), (unsigned)o.batch), dim3(256), 0, stream,
                        o, partial, parts, wide ? x : t, wide ? t : x, wide ? l.np : l.mp, wide ? l.mp : l.np);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
