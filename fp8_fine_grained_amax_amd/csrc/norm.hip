@@ -26,6 +26,10 @@ struct Raw8 {
             b = *reinterpret_cast<const uint4*>((const float*)p + i + 4);
         }
     }
+    // Hides that these are the values loaded, so that what was computed from them is computed again and not kept.
+    __device__ __forceinline__ void hide() {
+        asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w), "+v"(b.x), "+v"(b.y), "+v"(b.z), "+v"(b.w));
+    }
     __device__ __forceinline__ void get(float (&f)[8], int bf16) const {
         if (bf16) {
             unpack8(a, f);
@@ -50,43 +54,64 @@ __device__ __forceinline__ void store8(void* p, uint32_t i, const float (&f)[8],
     }
 }
 
-// Sum over the wave, in every lane: within the DPP rows (row_ror 8 and 4, quad_perm [2,3,0,1] and [1,0,3,2]), then across.
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the 16 lanes of a DPP row, in all of them (row_ror 8 and 4, quad_perm [2,3,0,1] and [1,0,3,2]).
+__device__ __forceinline__ float row16_sum(float v) {
 #define FG_STEP(ctrl) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false));
     FG_STEP(0x128)
     FG_STEP(0x124)
     FG_STEP(0x4E)
     FG_STEP(0xB1)
 #undef FG_STEP
-    return rows_sum(v);
+    return v;
 }
+__device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
 
-// The place of a workgroup's threads: `waves` to a row, so blockDim / (64 waves) rows at a time.
+constexpr int kMaxWaves = 16;
+// Threads of a workgroup whose threads hold U groups of eight columns each: with more groups a thread needs more registers
+// than 16 waves leave it.
+constexpr int max_waves(int u) { return u == 1 ? 16 : 12; }
+
+// The place of a workgroup's threads: `waves` to a row, so blockDim / (64 waves) rows at a time. Group u of thread t of a row
+// holds the columns 8 (t + 64 waves u) .. + 7.
 struct Place {
-    int wave, lane, group, groups, first, t;       // first: of the row's waves; t: thread of the row
-    __device__ __forceinline__ explicit Place(int waves) {
+    int wave, lane, group, groups, first, t, span, chunks;       // first: of the row's waves; chunks: a row's eights
+    __device__ __forceinline__ Place(int waves, int64_t cols) {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         lane = threadIdx.x & 63;
         group = wave / waves;
         first = group * waves;
         groups = (int)(blockDim.x >> 6) / waves;
         t = (int)threadIdx.x - first * 64;
+        span = 64 * waves;
+        chunks = (int)(cols / 8);
+    }
+    // Whether group u of U begins behind the row's end: only the last one can (the host takes no more waves than that needs).
+    template <int U>
+    __device__ __forceinline__ bool past(int u) const { return u + 1 == U && t + u * span >= chunks; }
+    template <int U>
+    __device__ __forceinline__ int wave_cols(int w) const {      // columns of the row's wave w
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int left = chunks - w * 64 - u * span;
+            n += 8 * (left < 0 ? 0 : left > 64 ? 64 : left);
+        }
+        return n;
     }
 };
 
-// Waves of a workgroup whose threads hold U groups of eight columns each: with more groups a thread needs more registers than
-// 16 waves leave it.
-constexpr int kMaxWaves = 16;
-constexpr int max_waves(int u) { return u <= 2 ? 16 : 12; }
-
 // ------------------------------------------------------------------------------------------------
-// Forward, tiles along the columns. U groups of eight columns a thread.
+// Forward, tiles along the columns. U groups of eight columns a thread, the next row's loaded while this one is worked on.
+//
+// FEW rows: a thread has as few groups as 16 waves a row allow, and gamma and beta in registers; a call's time is the latency
+// of its loads (one row of 1024: 2.3 us). Many: two groups (three past 16384 columns), so that what a row costs besides its elements (sums,
+// joins) is shared by more of them, and gamma and beta in LDS.
 // ------------------------------------------------------------------------------------------------
-template <int U, bool LAYER>
-__global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_kernel(FgNorm p, int waves, int64_t rows_each) {
+template <int U, bool XB, bool LAYER, bool FEW>
+__global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel(FgNorm p, int waves, int64_t rows_each) {
     __shared__ float part[2][kMaxWaves][2];         // a row's waves: sum, and sum of squares about the wave's mean
-    const Place at(waves);
-    const int chunks = (int)(p.cols / 8), span = 64 * waves;
+    extern __shared__ __attribute__((aligned(16))) float weights[];    // gamma, then beta
+    const Place at(waves, p.cols);
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int64_t end = row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
     const float n = (float)p.cols;
@@ -96,37 +121,59 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_kernel(FgNorm p, in
         row = row < end ? row : end - 1;
 #pragma unroll
         for (int u = 0; u < U; u++)
-            if (at.t + u * span < chunks) next[u].load(at_elem(p.x, row * p.ld, p.x_bf16), 8 * (at.t + u * span), p.x_bf16);
+            if (!at.past<U>(u)) next[u].load(at_elem(p.x, row * p.ld, XB), 8 * (at.t + u * at.span), XB);
     };
     load(row0 + at.group);
+    float gamma[FEW ? U : 1][8], beta[FEW ? U : 1][8];
+    auto weight = [&](const void* from, int c, float (&f)[8]) {
+        Raw8 w;
+        w.load(from, 8 * c, p.w_bf16);
+        w.get(f, p.w_bf16);
+    };
+    if constexpr (FEW) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (at.past<U>(u)) continue;
+            weight(p.gamma, at.t + u * at.span, gamma[u]);
+            if (p.beta) weight(p.beta, at.t + u * at.span, beta[u]);
+        }
+    } else {
+        for (int c = threadIdx.x; c < at.chunks; c += (int)blockDim.x) {
+            weight(p.gamma, c, gamma[0]);
+            store8(weights, 8 * c, gamma[0], 0);
+            if (p.beta) {
+                weight(p.beta, c, beta[0]);
+                store8(weights + p.cols, 8 * c, beta[0], 0);
+            }
+        }
+        __syncthreads();
+    }
+    float* scales[U];                               // of the lane's tiles, row 0
+#pragma unroll
+    for (int u = 0; u < U; u++) scales[u] = p.s_cols + (int64_t)((at.t + u * at.span) >> 4) * p.rows;
     int parity = 0;
     for (int64_t base = row0; base < end; base += at.groups, parity ^= 1) {
         const int64_t row = base + at.group;
         float v[U][8];
 #pragma unroll
-        for (int u = 0; u < U; u++) next[u].get(v[u], p.x_bf16);
+        for (int u = 0; u < U; u++) next[u].get(v[u], XB);
         load(row + at.groups);
 
         float sum = 0.0f, mean = 0.0f, square = 0.0f;
-        int own = 0;                                // the wave's columns
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int left = chunks - (at.wave - at.first) * 64 - u * span;
-            own += 8 * (left < 0 ? 0 : left > 64 ? 64 : left);
-        }
         if constexpr (LAYER) {
 #pragma unroll
             for (int u = 0; u < U; u++) {
-                if (at.t + u * span >= chunks) continue;
+                if (at.past<U>(u)) continue;
 #pragma unroll
                 for (int e = 0; e < 8; e++) sum += v[u][e];
             }
             sum = wave_sum(sum);
+            const int own = at.wave_cols<U>(at.wave - at.first);
             mean = own ? sum / (float)own : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            if (at.t + u * span >= chunks) continue;
+            if (at.past<U>(u)) continue;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float d = LAYER ? v[u][e] - mean : v[u][e];
@@ -140,25 +187,17 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_kernel(FgNorm p, in
                 part[parity][at.wave][1] = square;
             }
             __syncthreads();
-            if constexpr (LAYER) {
-                sum = 0.0f;
-                for (int w = 0; w < waves; w++) sum += part[parity][at.first + w][0];
-                mean = sum / n;
+            // each DPP row joins the waves' parts, one a lane
+            const int w = at.lane & 15;
+            const bool there = w < waves;
+            square = there ? part[parity][at.first + w][1] : 0.0f;
+            if constexpr (LAYER) {                  // about the row's mean instead of the wave's
+                const float s = there ? part[parity][at.first + w][0] : 0.0f;
+                mean = row16_sum(s) / n;
+                const float cols = (float)at.wave_cols<U>(w), d = there && cols > 0.0f ? s / cols - mean : 0.0f;
+                square = __builtin_fmaf(cols * d, d, square);
             }
-            square = 0.0f;
-            for (int w = 0; w < waves; w++) {
-                square += part[parity][at.first + w][1];
-                if constexpr (LAYER) {              // about the row's mean instead of the wave's
-                    int cols = 0;
-#pragma unroll
-                    for (int u = 0; u < U; u++) {
-                        const int left = chunks - w * 64 - u * span;
-                        cols += 8 * (left < 0 ? 0 : left > 64 ? 64 : left);
-                    }
-                    const float d = cols ? part[parity][at.first + w][0] / (float)cols - mean : 0.0f;
-                    square += (float)cols * d * d;
-                }
-            }
+            square = row16_sum(square);
         }
         if (row >= end) continue;
         const float var = square / n;
@@ -168,30 +207,52 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_kernel(FgNorm p, in
             if (LAYER && p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
+        float top[U], s[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int c = at.t + u * span;
-            if (c >= chunks) continue;              // whole DPP rows: cols is a multiple of 128
-            Raw8 w;
-            float gamma[8], beta[8], y[8];
-            w.load(p.gamma, 8 * c, p.w_bf16);
-            w.get(gamma, p.w_bf16);
+            const int c = at.t + u * at.span;
+            top[u] = 1.0f;                          // past the end: nothing, and no small scale
+            if (at.past<U>(u)) continue;            // whole DPP rows: cols is a multiple of 128
+            if constexpr (!FEW) {
+                const v4f a = *reinterpret_cast<const v4f*>(weights + 8 * c), b = *reinterpret_cast<const v4f*>(weights + 8 * c + 4);
 #pragma unroll
-            for (int e = 0; e < 8; e++) y[e] = (LAYER ? v[u][e] - mean : v[u][e]) * rstd;
+                for (int e = 0; e < 4; e++) gamma[0][e] = a[e], gamma[0][4 + e] = b[e];
+                if (p.beta) {
+                    const float* from = weights + (int)p.cols + 8 * c;
+                    const v4f d = *reinterpret_cast<const v4f*>(from), f = *reinterpret_cast<const v4f*>(from + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) beta[0][e] = d[e], beta[0][4 + e] = f[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[u][e] = (LAYER ? v[u][e] - mean : v[u][e]) * rstd;
             if (p.beta) {
-                w.load(p.beta, 8 * c, p.w_bf16);
-                w.get(beta, p.w_bf16);
 #pragma unroll
-                for (int e = 0; e < 8; e++) y[e] = __builtin_fmaf(y[e], gamma[e], beta[e]);
+                for (int e = 0; e < 8; e++) v[u][e] = __builtin_fmaf(v[u][e], gamma[FEW ? u : 0][e], beta[FEW ? u : 0][e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; e++) y[e] *= gamma[e];
+                for (int e = 0; e < 8; e++) v[u][e] *= gamma[FEW ? u : 0][e];
             }
-            const float s = fg_scale_from_amax(fg_row16_max(absmax8(y)), p.pow2);
-            const uint2 q = fg_any_small(s) ? quant8<true>(y, s) : quant8<false>(y, s);
-            *reinterpret_cast<uint2*>(p.q_cols + row * p.cols + 8 * (uint32_t)c) = q;
-            if ((c & 15) == 0) p.s_cols[(c >> 4) * p.rows + row] = s;
-            if (p.y) store8(p.y + row * p.cols, 8 * c, y, 1);
+            top[u] = fg_row16_max(absmax8(v[u]));
+        }
+        fg_scales_from_amax(top, p.pow2, s);
+        float least = s[0];
+#pragma unroll
+        for (int u = 1; u < U; u++) least = __builtin_fminf(least, s[u]);
+        const bool small = fg_any_small(least);
+        uint8_t* out = p.q_cols + row * p.cols;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = at.t + u * at.span;
+            if (at.past<U>(u)) continue;
+            const uint2 q = small ? quant8<true>(v[u], s[u]) : quant8<false>(v[u], s[u]);
+            *reinterpret_cast<uint2*>(out + 8 * (uint32_t)c) = q;
+            if ((at.t & 15) == 0) scales[u][row] = s[u];       // the span is a multiple of 64
+        }
+        if (p.y) {
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                if (!at.past<U>(u)) store8(p.y + row * p.cols, 8 * (at.t + u * at.span), v[u], 1);
         }
     }
 }
@@ -283,58 +344,110 @@ __global__ __launch_bounds__(512) void fg_norm_tokens_kernel(FgNorm p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Backward. The threads of a row as in the forward kernel; a workgroup's rows follow one another, and each thread adds up
-// its own columns' dy xhat and dy over them. The groups of a workgroup join in LDS, the workgroups in a second launch.
+// Backward. The threads of a row as in the forward kernel with few rows, and the next row's inputs loaded ahead as there; a
+// workgroup's rows follow one another, and each thread adds up its own columns' dy xhat and dy over them. The groups of a
+// workgroup join in LDS, the workgroups in a second launch.
 // ------------------------------------------------------------------------------------------------
-template <int U, bool LAYER>
+template <int U, bool LAYER, bool BIAS>
 __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBwd p, int waves, int64_t rows_each, int64_t partials) {
+    constexpr bool AHEAD = U == 1;                  // with more groups the registers do not hold a second row
     __shared__ float part[2][kMaxWaves][2];
-    extern __shared__ __attribute__((aligned(16))) float join[];       // [groups][cols], with more than one group
-    const Place at(waves);
-    const int chunks = (int)(p.cols / 8), span = 64 * waves;
+    constexpr bool HELD = U > 2;                    // the columns' sums are held in LDS, dgamma's and then dbeta's
+    extern __shared__ __attribute__((aligned(16))) float join[];       // else [groups][cols], with more than one group
+    const Place at(waves, p.cols);
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int64_t end = row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
     const float inv_n = 1.0f / (float)p.cols;
-    float dg[U][8], db[U][8];
+    // At.past, but asked of all groups after the first: the branches keep the compiler from working on all of them at once, for
+    // which it has too few registers.
+    auto behind = [&](int u) { return (u > 0 || U == 1) && at.t + u * at.span >= at.chunks; };
+    float dg[HELD ? 1 : U][8], db[BIAS && !HELD ? U : 1][8];
 #pragma unroll
-    for (int u = 0; u < U; u++)
+    for (int u = 0; u < U; u++) {
+        const float zero[8] = {};
+        if constexpr (HELD) {
+            if (behind(u)) continue;
+            store8(join, 8 * (at.t + u * at.span), zero, 0);
+            if constexpr (BIAS) store8(join + p.cols, 8 * (at.t + u * at.span), zero, 0);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; e++) dg[u][e] = db[u][e] = 0.0f;
+            for (int e = 0; e < 8; e++) dg[u][e] = db[BIAS ? u : 0][e] = 0.0f;
+        }
+    }
+    // adds to a thread's own columns of the sums in LDS
+    auto held = [&](float* sums, const float (&v)[8]) {
+        v4f* s = reinterpret_cast<v4f*>(sums);
+        s[0] += v4f{v[0], v[1], v[2], v[3]};
+        s[1] += v4f{v[4], v[5], v[6], v[7]};
+    };
 
-    int parity = 0;
-    for (int64_t base = row0; base < end; base += at.groups, parity ^= 1) {
-        const int64_t row = base + at.group < end ? base + at.group : end - 1;
-        const bool live = base + at.group < end;
-        const float rstd = p.rstd[row], mean = LAYER ? p.mean[row] : 0.0f;
-        Raw8 rx[U], rd[U];
+    Raw8 rx[U], rd[U], rr[AHEAD ? U : 1], nx[AHEAD ? U : 1], nd[AHEAD ? U : 1], nr[AHEAD ? U : 1];
+    float next_rstd, next_mean = 0.0f;
+    auto load = [&](int64_t row, Raw8* x, Raw8* d) {
+        row = row < end ? row : end - 1;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const uint32_t c = 8 * (at.t + u * span);
-            if (at.t + u * span >= chunks) continue;
-            rx[u].load(at_elem(p.x, row * p.ld_x, p.x_bf16), c, p.x_bf16);
-            rd[u].load(at_elem(p.dy, row * p.ld_dy, p.dy_bf16), c, p.dy_bf16);
+            const uint32_t c = 8 * (at.t + u * at.span);
+            if (behind(u)) continue;
+            x[u].load(at_elem(p.x, row * p.ld_x, p.x_bf16), c, p.x_bf16);
+            d[u].load(at_elem(p.dy, row * p.ld_dy, p.dy_bf16), c, p.dy_bf16);
+            if constexpr (AHEAD)
+                if (p.dres) nr[u].load(at_elem(p.dres, row * p.ld_dres, p.dres_bf16), c, p.dres_bf16);
         }
+        next_rstd = p.rstd[row];
+        if (LAYER) next_mean = p.mean[row];
+    };
+    float gamma[AHEAD ? U : 1][8];
+    auto load_gamma = [&](int u, float (&g)[8]) {
+        Raw8 w;
+        w.load(p.gamma, 8 * (at.t + u * at.span), p.w_bf16);
+        w.get(g, p.w_bf16);
+    };
+    if constexpr (AHEAD) {
+        load(row0 + at.group, nx, nd);
+        if (!behind(0)) load_gamma(0, gamma[0]);
+    }
+    int parity = 0;
+    for (int64_t base = row0; base < end; base += at.groups, parity ^= 1) {
+        const int64_t row = base + at.group;
+        const bool live = row < end;
+        if constexpr (AHEAD) {
+            rx[0] = nx[0];
+            rd[0] = nd[0];
+            rr[0] = nr[0];
+        } else {
+            load(row, rx, rd);
+        }
+        const float rstd = next_rstd, mean = next_mean;
+        if constexpr (AHEAD) load(row + at.groups, nx, nd);
         float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            if (at.t + u * span >= chunks) continue;
-            float x[8], d[8], gamma[8];
-            Raw8 w;
-            w.load(p.gamma, 8 * (at.t + u * span), p.w_bf16);
-            w.get(gamma, p.w_bf16);
+            if (behind(u)) continue;
+            float x[8], d[8];
+            if constexpr (!AHEAD) load_gamma(u, gamma[0]);
             rx[u].get(x, p.x_bf16);
             rd[u].get(d, p.dy_bf16);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                const float h = (LAYER ? x[e] - mean : x[e]) * rstd, t = d[e] * gamma[e];
-                if (live) {
-                    dg[u][e] = __builtin_fmaf(d[e], h, dg[u][e]);
-                    db[u][e] += d[e];
-                }
+                const float h = (LAYER ? x[e] - mean : x[e]) * rstd, t = d[e] * gamma[0][e];
+                x[e] = d[e] * h;
                 t1 += t;
                 t2 = __builtin_fmaf(t, h, t2);
             }
-            if constexpr (U > 2) __builtin_amdgcn_sched_barrier(0);    // the groups one after the other: registers
+            if (live) {
+                if constexpr (HELD) {
+                    held(join + 8 * (at.t + u * at.span), x);
+                    if constexpr (BIAS) held(join + p.cols + 8 * (at.t + u * at.span), d);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        dg[u][e] += x[e];
+                        if constexpr (BIAS) db[u][e] += d[e];
+                    }
+                }
+            }
+            if constexpr (U > 1) __builtin_amdgcn_sched_barrier(0);    // the groups one after the other: registers
         }
         t2 = wave_sum(t2);
         if constexpr (LAYER) t1 = wave_sum(t1);
@@ -344,48 +457,48 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
                 part[parity][at.wave][1] = t2;
             }
             __syncthreads();
-            t1 = t2 = 0.0f;
-            for (int w = 0; w < waves; w++) {
-                t1 += part[parity][at.first + w][0];
-                t2 += part[parity][at.first + w][1];
-            }
+            const int w = at.lane & 15;             // each DPP row joins the waves' parts, one a lane
+            t2 = row16_sum(w < waves ? part[parity][at.first + w][1] : 0.0f);
+            if constexpr (LAYER) t1 = row16_sum(w < waves ? part[parity][at.first + w][0] : 0.0f);
         }
         if (!live) continue;
         t1 *= inv_n;
         t2 *= inv_n;
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const uint32_t c = 8 * (at.t + u * span);
-            if (at.t + u * span >= chunks) continue;
-            float x[8], d[8], gamma[8], r[8];
-            Raw8 w;
-            w.load(p.gamma, c, p.w_bf16);
-            w.get(gamma, p.w_bf16);
+            const uint32_t c = 8 * (at.t + u * at.span);
+            if (behind(u)) continue;
+            float x[8], d[8], r[8];
+            if constexpr (!AHEAD) {
+                load_gamma(u, gamma[0]);
+                if (p.dres) rr[0].load(at_elem(p.dres, row * p.ld_dres, p.dres_bf16), c, p.dres_bf16);
+                rx[u].hide();
+                rd[u].hide();
+            }
             rx[u].get(x, p.x_bf16);
             rd[u].get(d, p.dy_bf16);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float h = (LAYER ? x[e] - mean : x[e]) * rstd;
-                const float t = __builtin_fmaf(d[e], gamma[e], LAYER ? -t1 : 0.0f);
+                const float t = __builtin_fmaf(d[e], gamma[0][e], LAYER ? -t1 : 0.0f);
                 d[e] = __builtin_fmaf(-h, t2, t) * rstd;
             }
             if (p.dres) {
-                w.load(at_elem(p.dres, row * p.ld_dres, p.dres_bf16), c, p.dres_bf16);
-                w.get(r, p.dres_bf16);
+                rr[0].get(r, p.dres_bf16);
 #pragma unroll
                 for (int e = 0; e < 8; e++) d[e] += r[e];
             }
             store8((char*)p.dx + (row * p.cols << (p.dx_bf16 ? 1 : 2)), c, d, p.dx_bf16);
-            if constexpr (U > 2) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (U > 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!p.partial) return;
-    auto put = [&](float (&v)[U][8], float* out) {
+    [[maybe_unused]] auto put = [&](auto& v, float* out) {
         if (at.groups > 1) {
             __syncthreads();
 #pragma unroll
             for (int u = 0; u < U; u++)
-                if (at.t + u * span < chunks) store8(join, at.group * (uint32_t)p.cols + 8 * (at.t + u * span), v[u], 0);
+                if (!behind(u)) store8(join, at.group * (uint32_t)p.cols + 8 * (at.t + u * at.span), v[HELD ? 0 : u], 0);
             __syncthreads();
             for (int c = threadIdx.x; c < (int)p.cols; c += (int)blockDim.x) {
                 float s = 0.0f;
@@ -395,11 +508,24 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
         } else {
 #pragma unroll
             for (int u = 0; u < U; u++)
-                if (at.t + u * span < chunks) store8(out, 8 * (at.t + u * span), v[u], 0);
+                if (!behind(u)) store8(out, 8 * (at.t + u * at.span), v[HELD ? 0 : u], 0);
         }
     };
-    if (p.dgamma) put(dg, p.partial + (int64_t)blockIdx.x * p.cols);
-    if (p.dbeta) put(db, p.partial + (partials + (int64_t)blockIdx.x) * p.cols);
+    float *out_g = p.partial + (int64_t)blockIdx.x * p.cols, *out_b = p.partial + (partials + (int64_t)blockIdx.x) * p.cols;
+    if constexpr (HELD) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = 8 * (at.t + u * at.span);
+            if (behind(u)) continue;
+            for (int e = 0; e < 8; e += 4) {
+                if (p.dgamma) *reinterpret_cast<v4f*>(out_g + c + e) = *reinterpret_cast<const v4f*>(join + c + e);
+                if constexpr (BIAS) *reinterpret_cast<v4f*>(out_b + c + e) = *reinterpret_cast<const v4f*>(join + p.cols + c + e);
+            }
+        }
+    } else {
+        if (p.dgamma) put(dg, out_g);
+        if constexpr (BIAS) put(db, out_b);
+    }
 }
 
 // Sums of the workgroups' partial sums: 64 columns a workgroup, the partials dealt to 16 waves in turn and the waves' sums
@@ -414,7 +540,13 @@ __global__ __launch_bounds__(kSumWaves * 64) void fg_norm_sum_kernel(const float
     if (!out) return;
     const float* from = partial + (int64_t)blockIdx.y * partials * cols;
     float s = 0.0f;
-    for (int64_t b = wave; b < partials; b += kSumWaves) s += from[b * cols + c];
+    for (int64_t b = wave; b < partials; b += 4 * kSumWaves) {     // four loads in flight
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = b + i * kSumWaves < partials ? from[(b + i * kSumWaves) * cols + c] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) s += v[i];
+    }
     sums[wave][lane] = s;
     __syncthreads();
     if (wave == 0) {
@@ -425,7 +557,7 @@ __global__ __launch_bounds__(kSumWaves * 64) void fg_norm_sum_kernel(const float
     }
 }
 
-// Groups of eight columns a thread and waves a row: as few groups as 16 waves (12 with three groups) allow.
+// Groups of eight columns a thread and waves a row: as few groups as 16 waves (12 with more than one) allow.
 int groups_of_thread(int64_t cols) {
     int u = 1;
     while (512 * u * max_waves(u) < cols) u++;
@@ -443,24 +575,48 @@ hipError_t by_groups(int64_t cols, Fn&& fn) {
     }
 }
 
+template <int U, bool FEW>
+hipError_t launch_fwd(const FgNorm& p, int waves, int groups, int64_t fill, hipStream_t stream) {
+    const int64_t each = ((p.rows + fill - 1) / fill + groups - 1) / groups * groups;
+    const unsigned grid = (unsigned)((p.rows + each - 1) / each), threads = 64u * waves * groups;
+    const int lds = FEW ? 0 : (int)p.cols * (p.beta ? 8 : 4);
+    auto go = [&](auto kern, std::atomic<uint64_t>& limit_set) {
+        if (lds > 0) {
+            const hipError_t e = fg_set_lds_limit_once((const void*)kern, (int)kFgNormMaxCols * 8, limit_set);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), lds, stream, p, waves, each);
+        return hipGetLastError();
+    };
+    static std::atomic<uint64_t> limits[4];
+    if (p.x_bf16) return p.layer ? go(fg_norm_kernel<U, true, true, FEW>, limits[0]) : go(fg_norm_kernel<U, true, false, FEW>, limits[1]);
+    return p.layer ? go(fg_norm_kernel<U, false, true, FEW>, limits[2]) : go(fg_norm_kernel<U, false, false, FEW>, limits[3]);
+}
+
 constexpr int64_t kMaxPartials = 256;
+// FEW and many measured, bf16 rows: 64 of 7168 4.3 and 4.5 us, 256 of 18432 6.8 and 7.2; 512 of 7168 6.6 and 6.0, 512 of 18432 11.7
+// and 9.7, 4096 of 7168 24.0 and 22.1.
+constexpr int64_t kFewRows = 256;
+
 int bwd_groups(int64_t cols) { return max_waves(groups_of_thread(cols)) / waves_of_row(cols); }
 
 }  // namespace
 
 hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
-    const int waves = waves_of_row(p.cols), groups = std::max(1, 4 / waves);
-    const unsigned threads = 64u * waves * groups;
-    const int64_t fill = (int64_t)fg_device_cus() * (2048 / threads);
-    int64_t each = (p.rows + fill - 1) / fill;
-    each = (each + groups - 1) / groups * groups;
-    const unsigned grid = (unsigned)((p.rows + each - 1) / each);
-    hipError_t e = by_groups(p.cols, [&](auto u) {
-        constexpr int U = decltype(u)::value;
-        if (p.layer) hipLaunchKernelGGL((fg_norm_kernel<U, true>), dim3(grid), dim3(threads), 0, stream, p, waves, each);
-        else hipLaunchKernelGGL((fg_norm_kernel<U, false>), dim3(grid), dim3(threads), 0, stream, p, waves, each);
-        return hipGetLastError();
-    });
+    const int64_t cus = fg_device_cus(), units = (p.cols + 511) / 512;
+    hipError_t e;
+    if (p.rows <= kFewRows) {
+        const int waves = waves_of_row(p.cols), groups = std::max(1, 4 / waves);
+        e = by_groups(p.cols, [&](auto u) { return launch_fwd<decltype(u)::value, true>(p, waves, groups, cus * (32 / (waves * groups)), stream); });
+    } else {
+        const int u = (int)std::min<int64_t>(units, units <= 32 ? 2 : 3), waves = (int)((units + u - 1) / u), groups = std::max(1, 4 / waves);
+        const int64_t fill = cus * std::max(1, 16 / (waves * groups));
+        switch (u) {
+            case 1: e = launch_fwd<1, false>(p, waves, groups, fill, stream); break;
+            case 2: e = launch_fwd<2, false>(p, waves, groups, fill, stream); break;
+            default: e = launch_fwd<3, false>(p, waves, groups, fill, stream); break;
+        }
+    }
     if (e != hipSuccess || !p.q_rows) return e;
     const unsigned tiles = (unsigned)((p.cols / FG_GROUP) * (p.rows / FG_GROUP));
     if (p.layer) hipLaunchKernelGGL((fg_norm_tokens_kernel<true>), dim3(tiles), dim3(512), 0, stream, p);
@@ -481,12 +637,22 @@ hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream) {
         const int64_t each = ((p.rows + most - 1) / most + groups - 1) / groups * groups;
         partials = (p.rows + each - 1) / each;
         const unsigned threads = 64u * waves * groups;
-        const size_t bytes = groups > 1 && p.partial ? (size_t)groups * (size_t)p.cols * 4 : 0;
+        // the groups' joins, or past 12288 columns the columns' sums
+        const bool held = groups_of_thread(p.cols) > 2;
+        const int bytes = (int)p.cols * 4 * (held ? (p.dbeta ? 2 : 1) : groups > 1 && p.partial ? groups : 0);
         const hipError_t e = by_groups(p.cols, [&](auto u) {
             constexpr int U = decltype(u)::value;
-            if (p.layer) hipLaunchKernelGGL((fg_norm_bwd_kernel<U, true>), dim3((unsigned)partials), dim3(threads), bytes, stream, p, waves, each, partials);
-            else hipLaunchKernelGGL((fg_norm_bwd_kernel<U, false>), dim3((unsigned)partials), dim3(threads), bytes, stream, p, waves, each, partials);
-            return hipGetLastError();
+            auto go = [&](auto kern, std::atomic<uint64_t>& limit_set) {
+                if (held) {
+                    const hipError_t e = fg_set_lds_limit_once((const void*)kern, (int)kFgNormMaxCols * 8, limit_set);
+                    if (e != hipSuccess) return e;
+                }
+                hipLaunchKernelGGL(kern, dim3((unsigned)partials), dim3(threads), bytes, stream, p, waves, each, partials);
+                return hipGetLastError();
+            };
+            static std::atomic<uint64_t> limits[4];
+            if (p.dbeta) return p.layer ? go(fg_norm_bwd_kernel<U, true, true>, limits[0]) : go(fg_norm_bwd_kernel<U, false, true>, limits[1]);
+            return p.layer ? go(fg_norm_bwd_kernel<U, true, false>, limits[2]) : go(fg_norm_bwd_kernel<U, false, false>, limits[3]);
         });
         if (e != hipSuccess) return e;
     }

@@ -9,6 +9,7 @@
 // from a transposed copy of X that the last product wrote beside X itself. The symmetric ones compute the tiles on and
 // below the diagonal and write each one twice. Contractions are padded with zeros to multiples of 64.
 #include "host_util.h"
+#include "ortho_shape.h"
 #include "train_launch.h"
 
 #include <algorithm>
@@ -156,8 +157,8 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
         uint16_t* out = p.out + batch * p.out_batch;
         const int width = p.bf16 ? p.N : (int)p.ld_out;
 #pragma unroll 4
-        for (int f = tid; f < BM * CH; f += THREADS) {
-            const int r = f / CH, c = f % CH;
+        for (int it = 0; it < BM * CH / THREADS; it++) {
+            const int f = it * THREADS + tid, r = f / CH, c = f % CH;
             if (m0 + r < p.M)
                 store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & MIX)) << 4)));
         }
@@ -166,9 +167,9 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
         constexpr int CH = BM / 8;
         uint16_t* out = p.out_t + batch * p.t_batch;
         const int width = p.bf16 ? p.M : (int)p.ld_t;
-#pragma unroll 2
-        for (int f = tid; f < BN * CH; f += THREADS) {
-            const int c0 = f / (16 * CH) * 16, r = 8 * (f / 16 % CH), col = c0 + 4 * (lrow & 3);     // column c0 + lrow, rows r .. r + 7
+#pragma unroll 4
+        for (int it = 0; it < BN * CH / THREADS; it++) {
+            const int f = it * THREADS + tid, c0 = f / (16 * CH) * 16, r = 8 * (f / 16 % CH), col = c0 + 4 * (lrow & 3);     // column c0 + lrow, rows r .. r + 7
             v2i part[2];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
@@ -189,7 +190,7 @@ struct MidTile {
 };
 
 template <int STAGES>
-__global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_gemm_kernel(OrthoGemm p) {
+__global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_kernel(OrthoGemm p) {
     using C = MidTile;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -622,39 +623,24 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
     }
 }
 
-int64_t tiles_of(const OrthoGemm& p, int side) {
-    const int64_t m = (p.M + side - 1) / side, n = (p.N + side - 1) / side;
-    return p.batch * (p.symmetric ? m * (m + 1) / 2 : m * n);
-}
-
-template <class Kernel>
-hipError_t launch(Kernel kern, std::atomic<uint64_t>& limit_set, int64_t tiles, int threads, int lds, const OrthoGemm& p, hipStream_t stream) {
+template <class Tile, class Kernel>
+hipError_t launch(Kernel kern, int side, int lds, std::atomic<uint64_t>& limit_set, const OrthoGemm& p, hipStream_t stream) {
     const hipError_t e = fg_set_lds_limit_once((const void*)kern, lds, limit_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(threads), lds, stream, p);
+    const unsigned tiles = (unsigned)ortho_tiles(p.batch, p.M, p.N, p.symmetric, side);
+    hipLaunchKernelGGL(kern, dim3(tiles), dim3(Tile::NTHREADS), lds, stream, p);
     return hipGetLastError();
 }
 
-template <int STAGES>
-hipError_t launch_mid(const OrthoGemm& p, hipStream_t stream) {
-    static std::atomic<uint64_t> limit_set{0};
-    return launch(fg_ortho_gemm_kernel<STAGES>, limit_set, tiles_of(p, 128), MidTile::NTHREADS, STAGES * MidTile::STAGE, p, stream);
-}
-
 hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
-    static std::atomic<uint64_t> limit_big{0}, limit_small{0};
-    const int64_t cus = fg_device_cus(), mid = tiles_of(p, 128), big = tiles_of(p, 256), small = tiles_of(p, 64);
-#ifdef FORCE
-    const char* f = getenv("FG_F");
-    if (f && *f == 's') return launch(fg_ortho_small_kernel, limit_small, small, SmallTile::NTHREADS, SmallTile::LDS, p, stream);
-    if (f && *f == 'b') return launch(fg_ortho_big_kernel, limit_big, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
-    if (f && *f == '4') return launch_mid<4>(p, stream);
-    if (f && *f == '2') return launch_mid<2>(p, stream);
-#endif
-    if ((big + cus - 1) / cus * 2.6 < (mid + 2 * cus - 1) / (2 * cus) * 2.0)
-        return launch(fg_ortho_big_kernel, limit_big, big, BigTile::NTHREADS, BigTile::LDS, p, stream);
-    if (small <= 2 * cus) return launch(fg_ortho_small_kernel, limit_small, small, SmallTile::NTHREADS, SmallTile::LDS, p, stream);
-    return mid <= cus ? launch_mid<4>(p, stream) : launch_mid<2>(p, stream);
+    static std::atomic<uint64_t> limits[4];
+    switch (ortho_tile(p.batch, p.M, p.N, p.symmetric, p.ld / BK, fg_device_cus())) {
+        case TILE_64: return launch<SmallTile>(fg_ortho_small_kernel, 64, SmallTile::LDS, limits[0], p, stream);
+        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<4>, 128, 4 * MidTile::STAGE, limits[1], p, stream);
+        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<2>, 128, 2 * MidTile::STAGE, limits[2], p, stream);
+        case TILE_256: break;
+    }
+    return launch<BigTile>(fg_ortho_big_kernel, 256, BigTile::LDS, limits[3], p, stream);
 }
 
 // The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.

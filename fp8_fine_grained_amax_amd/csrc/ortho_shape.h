@@ -1,0 +1,57 @@
+// Host arithmetic of the Newton-Schulz products: which workgroup tile a product gets. No HIP: fitted to times measured on the
+// 256 CUs of an MI355X.
+#pragma once
+#include <stdint.h>
+
+namespace {
+
+enum OrthoTile { TILE_64, TILE_128, TILE_128_PAIRS, TILE_256 };      // PAIRS: two workgroups to a CU, with half the stages
+
+// Tiles of a batch of M x N products; a symmetric one computes those on and below the diagonal.
+inline int64_t ortho_tiles(int64_t batch, int64_t M, int64_t N, bool symmetric, int side) {
+    const int64_t m = (M + side - 1) / side, n = (N + side - 1) / side;
+    return batch * (symmetric ? m * (m + 1) / 2 : m * n);
+}
+
+// Estimated time in us of a product whose contraction has `steps` steps of 64: rounds of tiles over the CUs, each with a fixed
+// part (first loads, last stores) and a time for every step that grows with the CUs that are busy (they share caches
+// and power). Measured and (estimated), five symmetric products and four others:
+//                                    64            128          128 in pairs   256
+//   256 x 256, 16 steps              8.2 (8.7)     13.7 (15)    13.6 (16)      22.5 (27)
+//   1024 x 1024, 64                  16.2 (17)     33.8 (35)    41.2 (39)      68.2 (70)
+//   2048 x 2048, 32                  32.4 (37)     22.0 (24)    25.6 (26)      42.3 (44)
+//   4096 x 4096, 64                  186 (175)     111 (116)    98.1 (108)     82.2 (90)
+//   8 of 2048 x 2048, 32             -             120 (115)    101 (100)      111 (105)
+//   1000 x 2001, 16                  16.7 (18)     16.7 (16)    17.9 (17)      32.8 (29)
+//   1536 x 4096, 24                  56.9 (62)     38.2 (39)    31.4 (29)      39.7 (42)
+//   8 of 1024 x 2048, 16             101 (134)     60.2 (60)    46.8 (47)      39.6 (43)
+//   8 of 2048 x 7168, 32             -             705 (650)    606 (535)      434 (433)
+inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_t cus) {
+    const int64_t slots = tile == TILE_128_PAIRS ? 2 * cus : cus;
+    auto round = [&](double fill) {
+        const double s = (double)steps;
+        switch (tile) {
+            case TILE_64: return 4.6 + (tiles > cus ? 0.23 : 0.17) * s;
+            case TILE_128: return 5.5 + (0.39 + 0.16 * fill) * s;
+            case TILE_128_PAIRS: return 6.0 + (fill <= 0.5 ? 0.45 + 0.3 * fill : 0.7 + 0.6 * (fill - 0.5)) * s;
+            default: return 9.5 + 7.0 * fill + (0.85 + 0.55 * fill) * s;
+        }
+    };
+    const int64_t whole = tiles / slots, rest = tiles % slots;
+    return (tile == TILE_64 ? 1.4 : tile == TILE_256 ? 4.0 : 3.0) + (double)whole * round(1.0) +
+           (rest ? round((double)rest / (double)slots) : 0.0);
+}
+
+inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus) {
+    const OrthoTile shapes[] = {TILE_64, TILE_128, TILE_128_PAIRS, TILE_256};
+    const int sides[] = {64, 128, 128, 256};
+    OrthoTile best = TILE_64;
+    double least = 0.0;
+    for (int i = 0; i < 4; i++) {
+        const double us = ortho_tile_us(shapes[i], ortho_tiles(batch, M, N, symmetric, sides[i]), steps, cus);
+        if (i == 0 || us < least) best = shapes[i], least = us;
+    }
+    return best;
+}
+
+}  // namespace

@@ -13,6 +13,7 @@ constexpr int64_t kMaxRows = 1LL << 25;
 constexpr int64_t kMaxStride = 1LL << 40;
 constexpr int64_t kMaxSide = 65536;              // of a weight: 32-bit offsets inside a tile of its padded copies
 constexpr int64_t kMaxBlocks = (1LL << 24) - 1;  // 64 x 64 blocks of all matrices: a launch has less than 2^32 threads
+constexpr int64_t kMaxBatch = 65535;             // a grid's y
 constexpr int kMaxSteps = 32;
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -54,7 +55,7 @@ bool in_range(double a, double b, double c, int steps) {
 }
 
 bool side_ok(int64_t batch, int64_t N, int64_t K) {
-    return N <= kMaxSide && K <= kMaxSide && batch <= kMaxBlocks / (cdiv(N, 64) * cdiv(K, 64));
+    return N <= kMaxSide && K <= kMaxSide && batch <= kMaxBatch && batch <= kMaxBlocks / (cdiv(N, 64) * cdiv(K, 64));
 }
 
 }  // namespace

@@ -79,7 +79,7 @@ fg_status fg_norm_bwd(const void* x, fg_out_dtype x_type, int64_t ld_x, const fl
  *   2.0315) does, for any steps.
  *   A matrix of zeros gives zeros; one that holds a NaN or an infinity, or whose norm overflows fp32, gives NaN.
  *   workspace  fg_orthogonalize_workspace(batch, N, K) bytes, 256-byte aligned; 0 for sizes that are refused here.
- *   N and K at most 65536, batch * ceil(N / 64) * ceil(K / 64) < 2^24, 1 <= steps <= 32, a, b, c, eps and scale finite, eps >
+ *   N and K at most 65536, batch at most 65535, batch * ceil(N / 64) * ceil(K / 64) < 2^24, 1 <= steps <= 32, a, b, c, eps and scale finite, eps >
  *   0. g aligned to its elements, out 2-byte aligned. batch, N or K == 0 is a no-op. The workspace must not overlap g or out;
  *   out may be g itself only where nothing else of g's storage is needed: other overlaps are undefined. */
 int64_t fg_orthogonalize_workspace(int64_t batch, int64_t N, int64_t K);

@@ -58,7 +58,7 @@ def filled(rows, cols, layer, tokens, y=True):
                         f32(rows) if layer else None, f32(rows))
 
 
-NORM_SHAPES = [(1, 128), (1, 1024), (3, 384), (5, 640), (17, 512), (2, 8192), (33, 7168), (4, 8320), (3, 16384), (2, 16512), (3, 18432),
+NORM_SHAPES = [(1, 128), (1, 1024), (3, 384), (5, 640), (17, 512), (2, 8192), (33, 7168), (4, 8320), (3, 12288), (3, 12416), (3, 16384), (2, 16512), (3, 18432),
                (700, 256), (1200, 1152), (600, 4224)]
 
 
