@@ -37,6 +37,7 @@ struct OrthoGemm {
     int M, N, batch;
     float alpha, beta;
     int symmetric;                               // out and out_t are the same matrix
+    int first, count;                            // the 256 x 256 tiles to compute, on tiles of 128 in quarters; count 0: everything
     int bf16;                                    // outputs are bf16 without padding; fp16 with zeros up to their strides if not
 };
 
@@ -78,6 +79,21 @@ __device__ __forceinline__ void triangle(int id, int& i, int& j) {
 // them in lane l: the chunks 2 (l / 16) in one operand and 2 (l / 16) + 1 in the other, for both sides alike. (The order of a
 // contraction is free. With l / 16 and l / 16 + 4 every read had a two-way bank conflict, 5% of the time.)
 __device__ __forceinline__ int frag_at(int row, int c) { return row * 128 + ((c ^ swz128(row)) << 4); }
+
+// The 256 x 256 tile number id of a batch.
+__device__ __forceinline__ void big_tile(const OrthoGemm& p, int id, int64_t& batch, int& ti, int& tj) {
+    const int m_tiles = (p.M + 255) / 256, n_tiles = (p.N + 255) / 256;
+    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles, local = id % per;
+    batch = id / per;
+    if (p.symmetric) {
+        triangle(local, ti, tj);
+    } else {
+        constexpr int GM = 8;                            // rows of tiles that an XCD's run goes down together
+        const int group = local / (GM * n_tiles), first = group * GM, rows = min(m_tiles - first, GM), within = local - group * GM * n_tiles;
+        ti = first + within % rows;
+        tj = within / rows;
+    }
+}
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -197,11 +213,20 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     const int wm = wave >> 1, wn = wave & 1;
     const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
     const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
-    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
-    const int64_t batch = id / per;
     int ti, tj;
-    if (p.symmetric) triangle(local, ti, tj);
-    else ti = local % m_tiles, tj = local / m_tiles;
+    int64_t batch;
+    if (p.count) {                                       // quarters of 256 x 256 tiles
+        const int id = xcd_remap((int)blockIdx.x, 4 * p.count);
+        big_tile(p, p.first + (id >> 2), batch, ti, tj);
+        ti = 2 * ti + (id >> 1 & 1);
+        tj = 2 * tj + (id & 1);
+        if (ti >= m_tiles || tj >= n_tiles || (p.symmetric && tj > ti)) return;
+    } else {
+        const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
+        batch = id / per;
+        if (p.symmetric) triangle(local, ti, tj);
+        else ti = local % m_tiles, tj = local / m_tiles;
+    }
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
     const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
     const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
@@ -311,19 +336,9 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
-    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
-    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
-    const int64_t batch = id / per;
+    int64_t batch;
     int ti, tj;
-    if (p.symmetric) {
-        triangle(local, ti, tj);
-    } else {
-        constexpr int GM = 8;                            // rows of tiles that an XCD's run goes down together
-        const int group = local / (GM * n_tiles), first = group * GM, rows = min(m_tiles - first, GM), within = local - group * GM * n_tiles;
-        ti = first + within % rows;
-        tj = within / rows;
-    }
+    big_tile(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
     const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
     const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
@@ -630,23 +645,36 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
 }
 
 template <class Tile, class Kernel>
-hipError_t launch(Kernel kern, int side, int lds, std::atomic<uint64_t>& limit_set, const OrthoGemm& p, hipStream_t stream) {
+hipError_t launch(Kernel kern, int64_t tiles, int lds, std::atomic<uint64_t>& limit_set, const OrthoGemm& p, hipStream_t stream) {
     const hipError_t e = fg_set_lds_limit_once((const void*)kern, lds, limit_set);
     if (e != hipSuccess) return e;
-    const unsigned tiles = (unsigned)ortho_tiles(p.batch, p.M, p.N, p.symmetric, side);
-    hipLaunchKernelGGL(kern, dim3(tiles), dim3(Tile::NTHREADS), lds, stream, p);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(Tile::NTHREADS), lds, stream, p);
     return hipGetLastError();
 }
 
-hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
+hipError_t launch_tile(OrthoTile tile, const OrthoGemm& p, hipStream_t stream) {
     static std::atomic<uint64_t> limits[4];
-    switch (ortho_tile(p.batch, p.M, p.N, p.symmetric, p.ld / BK, fg_device_cus())) {
-        case TILE_64: return launch<SmallTile>(fg_ortho_small_kernel, 64, SmallTile::LDS, limits[0], p, stream);
-        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<4>, 128, 4 * MidTile::STAGE, limits[1], p, stream);
-        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<2>, 128, 2 * MidTile::STAGE, limits[2], p, stream);
-        case TILE_256: break;
+    auto tiles = [&](int side) { return ortho_tiles(p.batch, p.M, p.N, p.symmetric, side); };
+    const int64_t quarters = p.count ? 4 * (int64_t)p.count : tiles(128);
+    switch (tile) {
+        case TILE_64: return launch<SmallTile>(fg_ortho_small_kernel, tiles(64), SmallTile::LDS, limits[0], p, stream);
+        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<4>, quarters, 4 * MidTile::STAGE, limits[1], p, stream);
+        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<2>, quarters, 2 * MidTile::STAGE, limits[2], p, stream);
+        default: return launch<BigTile>(fg_ortho_big_kernel, p.count ? p.count : tiles(256), BigTile::LDS, limits[3], p, stream);
     }
-    return launch<BigTile>(fg_ortho_big_kernel, 256, BigTile::LDS, limits[3], p, stream);
+}
+
+hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
+    const int64_t cus = fg_device_cus();
+    const OrthoTile tile = ortho_tile(p.batch, p.M, p.N, p.symmetric, p.ld / BK, cus);
+    if (tile != TILE_256_TAIL) return launch_tile(tile, p, stream);
+    const int64_t all = ortho_tiles(p.batch, p.M, p.N, p.symmetric, 256), rest = all % cus;
+    OrthoGemm part = p;
+    part.count = (int)(all - rest);
+    if (const hipError_t e = launch_tile(TILE_256, part, stream); e != hipSuccess) return e;
+    part.first = part.count;
+    part.count = (int)rest;
+    return launch_tile(ortho_tail_tile(rest, cus), part, stream);
 }
 
 // The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.

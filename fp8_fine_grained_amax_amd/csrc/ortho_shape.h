@@ -5,7 +5,8 @@
 
 namespace {
 
-enum OrthoTile { TILE_64, TILE_128, TILE_128_PAIRS, TILE_256 };      // PAIRS: two workgroups to a CU, with half the stages
+// PAIRS: two workgroups to a CU, with half the stages. TAIL: whole rounds of 256, and the rest in quarters of 128.
+enum OrthoTile { TILE_64, TILE_128, TILE_128_PAIRS, TILE_256, TILE_256_TAIL };
 
 // Tiles of a batch of M x N products; a symmetric one computes those on and below the diagonal.
 inline int64_t ortho_tiles(int64_t batch, int64_t M, int64_t N, bool symmetric, int side) {
@@ -42,6 +43,10 @@ inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_
            (rest ? round((double)rest / (double)slots) : 0.0);
 }
 
+// The rest of whole rounds of 256 x 256 tiles, in quarters on 128 x 128 tiles, one or two to a CU. Eight symmetric 2048 x 2048
+// (288 tiles), 112 steps: 250 us in two launches and 301 in one; 32 steps: 91 and 111 (101 on 128 x 128 tiles alone).
+inline OrthoTile ortho_tail_tile(int64_t rest, int64_t cus) { return 4 * rest <= cus ? TILE_128 : TILE_128_PAIRS; }
+
 inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus) {
     const OrthoTile shapes[] = {TILE_64, TILE_128, TILE_128_PAIRS, TILE_256};
     const int sides[] = {64, 128, 128, 256};
@@ -50,6 +55,11 @@ inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric,
     for (int i = 0; i < 4; i++) {
         const double us = ortho_tile_us(shapes[i], ortho_tiles(batch, M, N, symmetric, sides[i]), steps, cus);
         if (i == 0 || us < least) best = shapes[i], least = us;
+    }
+    const int64_t big = ortho_tiles(batch, M, N, symmetric, 256), rest = big % cus;
+    if (big > cus && rest > 0) {
+        const double us = ortho_tile_us(TILE_256, big - rest, steps, cus) + ortho_tile_us(ortho_tail_tile(rest, cus), 4 * rest, steps, cus);
+        if (us < least) best = TILE_256_TAIL;
     }
     return best;
 }

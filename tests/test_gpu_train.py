@@ -293,6 +293,19 @@ def test_update_batches_and_strides(shape):
     assert torch.equal(fg.fg_orthogonalize(g[0]), out[0])
 
 
+@pytest.mark.parametrize("batch,n,k,steps", [(1, 1100, 4200, 2), (3, 1030, 2100, 2), (1, 4096, 4160, 1), (8, 2048, 2048, 2), (9, 2050, 1990, 1)])
+def test_update_on_every_tile(batch, n, k, steps):
+    """Sizes whose products take the 128 x 128 tiles in both forms, the 256 x 256 ones, and those with a rest in quarters, whose
+    matrices are the last."""
+    g = torch.stack([gradient(i, n, k) for i in range(batch)])
+    out = fg.fg_orthogonalize(g, steps=steps, out=torch.full((batch, n, k), float("nan"), dtype=torch.bfloat16, device=device()),
+                              workspace=dirty_workspace(batch, n, k))
+    assert bool(torch.isfinite(out).all())
+    for i in {0, batch // 2, batch - 1}:
+        ref.check_update(out[i], *ref.orthogonalize(g[i].double(), steps=steps), (n, k, i))
+    assert torch.equal(fg.fg_orthogonalize(g, steps=steps), out)
+
+
 def test_update_special_matrices():
     """Zeros give zeros, whatever stands beside; a NaN or an infinity stays in its own matrix; scales far from one do not matter."""
     g = torch.stack([gradient(i, 100, 150) for i in range(5)])
