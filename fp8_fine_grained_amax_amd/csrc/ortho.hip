@@ -442,15 +442,20 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
 
 // ------------------------------------------------------------------------------------------------
 // 64 x 64 workgroup tiles for small matrices: 4 waves, each with a quarter of the contraction (every fourth K step) for the whole
-// tile and a ring of two stages of its own, so that nothing waits for another wave before the sums are joined, in LDS and in
-// the order of the waves.
+// tile and stages of its own, so that nothing waits for another wave before the sums are joined, in LDS and in the order of
+// the waves. A CU loads at about 80 to 95 GB/s, and that bounds the K steps: two stages a wave (SLOTS) gain only 5 to 8% over
+// one, which leaves room for a second workgroup on a CU: 256 x 256 x 1024, 10 tiles, 7.8 and 8.3 us; 1000 x 2001 x 1000, 512
+// tiles, 16.0 and 13.6.
 // ------------------------------------------------------------------------------------------------
+template <int SLOTS_>
 struct SmallTile {
-    static constexpr int NTHREADS = 256, WAVES = 4, SIDE = 64, SUB = 4, STAGE = 2 * SIDE * 128, LOADS = 16, LDS = WAVES * 2 * STAGE;
+    static constexpr int SLOTS = SLOTS_, NTHREADS = 256, WAVES = 4, SIDE = 64, SUB = 4, STAGE = 2 * SIDE * 128, LOADS = 16;
+    static constexpr int LDS = SLOTS == 2 ? WAVES * 2 * STAGE : WAVES * STAGE + 8192;
 };
 
-__global__ __launch_bounds__(SmallTile::NTHREADS, 1) void fg_ortho_small_kernel(OrthoGemm p) {
-    using C = SmallTile;
+template <int SLOTS>
+__global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGemm p) {
+    using C = SmallTile<SLOTS>;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m_tiles = (p.M + C::SIDE - 1) / C::SIDE, n_tiles = (p.N + C::SIDE - 1) / C::SIDE;
@@ -463,7 +468,7 @@ __global__ __launch_bounds__(SmallTile::NTHREADS, 1) void fg_ortho_small_kernel(
     const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = (int)(p.ld / BK);
     const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
     const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
-    uint8_t* ring = smem + wave * (2 * C::STAGE);
+    uint8_t* ring = smem + wave * (SLOTS * C::STAGE);
 
     uint32_t a_off[8], b_off[8];
 #pragma unroll
@@ -494,10 +499,10 @@ __global__ __launch_bounds__(SmallTile::NTHREADS, 1) void fg_ortho_small_kernel(
     load_e(p, e, batch, m0, n0, 16 * wave, 0);
     __builtin_amdgcn_sched_barrier(0);
     issue(wave, 0);
-    issue(wave + C::WAVES, 1);
+    if constexpr (SLOTS == 2) issue(wave + C::WAVES, 1);
     int slot = 0;
-    for (int kb = wave; kb < nkb; kb += C::WAVES, slot ^= 1) {
-        if (kb + C::WAVES < nkb) wait_loads<C::LOADS>(); // this step's, with the next one's outstanding
+    for (int kb = wave; kb < nkb; kb += C::WAVES, slot ^= SLOTS - 1) {
+        if (SLOTS == 2 && kb + C::WAVES < nkb) wait_loads<C::LOADS>(); // this step's, with the next one's outstanding
         else wait_loads<0>();
         __builtin_amdgcn_sched_barrier(0);
         const uint8_t* st = ring + slot * C::STAGE;
@@ -511,7 +516,7 @@ __global__ __launch_bounds__(SmallTile::NTHREADS, 1) void fg_ortho_small_kernel(
             }
         __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the slot is read
         __builtin_amdgcn_sched_barrier(0);
-        issue(kb + 2 * C::WAVES, slot);
+        issue(kb + SLOTS * C::WAVES, slot);
 #pragma unroll
         for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -653,11 +658,13 @@ hipError_t launch(Kernel kern, int64_t tiles, int lds, std::atomic<uint64_t>& li
 }
 
 hipError_t launch_tile(OrthoTile tile, const OrthoGemm& p, hipStream_t stream) {
-    static std::atomic<uint64_t> limits[4];
+    static std::atomic<uint64_t> limits[5];
     auto tiles = [&](int side) { return ortho_tiles(p.batch, p.M, p.N, p.symmetric, side); };
     const int64_t quarters = p.count ? 4 * (int64_t)p.count : tiles(128);
     switch (tile) {
-        case TILE_64: return launch<SmallTile>(fg_ortho_small_kernel, tiles(64), SmallTile::LDS, limits[0], p, stream);
+        case TILE_64:
+            if (tiles(64) <= fg_device_cus()) return launch<SmallTile<2>>(fg_ortho_small_kernel<2>, tiles(64), SmallTile<2>::LDS, limits[0], p, stream);
+            return launch<SmallTile<1>>(fg_ortho_small_kernel<1>, tiles(64), SmallTile<1>::LDS, limits[4], p, stream);
         case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<4>, quarters, 4 * MidTile::STAGE, limits[1], p, stream);
         case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<2>, quarters, 2 * MidTile::STAGE, limits[2], p, stream);
         default: return launch<BigTile>(fg_ortho_big_kernel, p.count ? p.count : tiles(256), BigTile::LDS, limits[3], p, stream);

@@ -18,29 +18,32 @@ inline int64_t ortho_tiles(int64_t batch, int64_t M, int64_t N, bool symmetric, 
 // part (first loads, last stores) and a time for every step that grows with the CUs that are busy (they share caches
 // and power). Measured and (estimated), five symmetric products and four others:
 //                                    64            128          128 in pairs   256
-//   256 x 256, 16 steps              8.2 (8.7)     13.7 (15)    13.6 (16)      22.5 (27)
-//   1024 x 1024, 64                  16.2 (17)     33.8 (35)    41.2 (39)      68.2 (70)
-//   2048 x 2048, 32                  32.4 (37)     22.0 (24)    25.6 (26)      42.3 (44)
-//   4096 x 4096, 64                  186 (175)     111 (116)    98.1 (108)     82.2 (90)
+//   256 x 256, 16 steps              7.8 (8.7)     13.7 (15)    13.6 (16)      22.5 (27)
+//   1024 x 1024, 64                  15.8 (17)     33.8 (35)    41.2 (39)      68.2 (70)
+//   2048 x 2048, 32                  23.8 (24)     22.0 (24)    25.6 (26)      42.3 (44)
+//   4096 x 4096, 64                  163 (165)     111 (116)    98.1 (108)     82.2 (90)
 //   8 of 2048 x 2048, 32             -             120 (115)    101 (100)      111 (105)
-//   1000 x 2001, 16                  16.7 (18)     16.7 (16)    17.9 (17)      32.8 (29)
-//   1536 x 4096, 24                  56.9 (62)     38.2 (39)    31.4 (29)      39.7 (42)
-//   8 of 1024 x 2048, 16             101 (134)     60.2 (60)    46.8 (47)      39.6 (43)
+//   1000 x 2001, 16                  13.6 (13)     16.7 (16)    17.9 (17)      32.8 (29)
+//   1536 x 4096, 24                  41.5 (52)     38.2 (39)    31.4 (29)      39.7 (42)
+//   8 of 1024 x 2048, 16             70.0 (100)    60.2 (60)    46.8 (47)      39.6 (43)
 //   8 of 2048 x 7168, 32             -             705 (650)    606 (535)      434 (433)
 inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_t cus) {
+    const double s = (double)steps;
+    if (tile == TILE_64) {                       // one workgroup a CU, or two
+        if (tiles <= cus) return 6.0 + 0.17 * s;
+        const double fill = (double)tiles / (double)(2 * cus);
+        return fill <= 1.0 ? 4.5 + (0.2 + 0.3 * fill) * s : 1.5 + fill * (3.0 + 0.58 * s);
+    }
     const int64_t slots = tile == TILE_128_PAIRS ? 2 * cus : cus;
     auto round = [&](double fill) {
-        const double s = (double)steps;
         switch (tile) {
-            case TILE_64: return 4.6 + (tiles > cus ? 0.23 : 0.17) * s;
             case TILE_128: return 5.5 + (0.39 + 0.16 * fill) * s;
             case TILE_128_PAIRS: return 6.0 + (fill <= 0.5 ? 0.45 + 0.3 * fill : 0.7 + 0.6 * (fill - 0.5)) * s;
             default: return 9.5 + 7.0 * fill + (0.85 + 0.55 * fill) * s;
         }
     };
     const int64_t whole = tiles / slots, rest = tiles % slots;
-    return (tile == TILE_64 ? 1.4 : tile == TILE_256 ? 4.0 : 3.0) + (double)whole * round(1.0) +
-           (rest ? round((double)rest / (double)slots) : 0.0);
+    return (tile == TILE_256 ? 4.0 : 3.0) + (double)whole * round(1.0) + (rest ? round((double)rest / (double)slots) : 0.0);
 }
 
 // The rest of whole rounds of 256 x 256 tiles, in quarters on 128 x 128 tiles, one or two to a CU. Eight symmetric 2048 x 2048

@@ -1,0 +1,60 @@
+"""The tile that a Newton-Schulz product gets, without a GPU: the estimates against times measured on an MI355X (us), and that the
+choice is near the fastest."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+
+# batch, M, N, symmetric, steps: measured on tiles of 64, 128, 128 in pairs and 256
+MEASURED = {(1, 256, 256, 1, 16): (7.8, 13.7, 13.6, 22.5), (1, 256, 256, 1, 4): (5.0, 9.7, 9.2, 16.3), (1, 256, 1024, 0, 4): (5.1, 9.0, 8.8, 17.1),
+            (1, 1000, 1000, 1, 32): (10.9, 20.6, 23.4, 40.8), (1, 1000, 2001, 0, 16): (13.6, 16.7, 17.9, 32.8),
+            (1, 512, 512, 1, 8): (6.6, 10.2, 10.5, 19.4), (1, 1024, 1024, 1, 64): (15.8, 33.8, 41.2, 68.2),
+            (1, 1024, 4096, 0, 16): (21.0, 17.4, 18.0, 30.3), (1, 2048, 2048, 1, 32): (23.8, 22.0, 25.6, 42.3),
+            (1, 2048, 2048, 0, 32): (39.4, 25.8, 28.6, 45.5), (1, 1536, 1536, 1, 64): (26.8, 34.8, 42.3, 69.7),
+            (1, 1536, 4096, 0, 24): (41.5, 38.2, 31.4, 39.7), (8, 512, 512, 1, 16): (10.2, 13.8, 13.1, 26.8),
+            (8, 1024, 1024, 1, 32): (35.8, 41.0, 32.3, 44.6), (8, 1024, 2048, 0, 16): (70.0, 60.2, 46.8, 39.6),
+            (1, 4096, 4096, 1, 64): (163, 111, 98.1, 82.2), (1, 4096, 4096, 0, 64): (304, 175, 133, 105.6),
+            (8, 2048, 7168, 0, 32): (None, 705, 606, 434)}
+
+
+@pytest.fixture(scope="module")
+def ask(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("ortho") / "driver")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined", "-I",
+                        os.path.join(ROOT, "fp8_fine_grained_amax_amd", "csrc"), os.path.join(ROOT, "tests", "ortho_shape_driver.cpp"),
+                        "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+    def run(problems):
+        text = "".join(" ".join(map(str, p)) + "\n" for p in problems)
+        r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60, env=dict(os.environ, ASAN_OPTIONS="verify_asan_link_order=0"))
+        assert r.returncode == 0 and "runtime error" not in r.stderr, r.stderr
+        lines = [line.split() for line in r.stdout.splitlines()]
+        return [(int(v[0]), [float(x) for x in v[1:]]) for v in lines]
+    return run
+
+
+def test_estimates_and_choices(ask):
+    for (problem, measured), (choice, us) in zip(MEASURED.items(), ask(list(MEASURED))):
+        for m, e in zip(measured, us):
+            assert m is None or 0.65 < e / m < 1.5, (problem, measured, us)
+        fastest = min(m for m in measured if m is not None)
+        assert choice < 4 and measured[choice] <= 1.1 * fastest, (problem, choice, measured)
+
+
+def test_rest_of_a_round(ask):
+    # 288 tiles of 256: one round, and 32 tiles in quarters; 256 and 136 tiles have no whole round with a rest
+    (tail, _), (even, _), (few, _) = ask([(8, 2048, 2048, 1, 112), (1, 4096, 4096, 0, 64), (1, 4096, 4096, 1, 64)])
+    assert (tail, even, few) == (4, 3, 3)
+
+
+def test_every_size_has_a_choice(ask):
+    sides = (1, 2, 63, 64, 65, 129, 500, 1000, 3000, 8191, 20000, 65536)
+    problems = [(b, m, n, int(m == n), (n + 63) // 64) for b in (1, 7, 300, 65535) for m in sides for n in sides
+                if m <= n and b * ((m + 63) // 64) * ((n + 63) // 64) < 1 << 24]
+    for problem, (choice, us) in zip(problems, ask(problems)):
+        assert 0 <= choice <= 4 and all(u > 0 for u in us), problem
