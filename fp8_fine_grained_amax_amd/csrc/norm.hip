@@ -1,8 +1,11 @@
 // Layer and RMS norm whose output leaves as FP8 tiles, and their backward pass (gfx950). Both are bound by HBM.
 //
 // A row's threads hold it in registers, eight neighbouring columns a thread and group, so a 1x128 tile is 16 lanes (one
-// DPP row) and x is read once for statistics, tiles and output. Rows that a workgroup takes follow one another, so that the
-// scales it writes (rows contiguous) meet in lines of its own L2.
+// DPP row). With tiles along the columns only, one kernel reads x once for statistics, tiles and output. Tiles along the rows
+// need the statistics of 128 rows, which no workgroup holds: there one kernel makes the statistics, and a second one reads x
+// again in 128 x 128 blocks and writes both tilings. (Columns' tiles in the first kernel and rows' tiles in the second write
+// the same bytes, but with the first kernel's scales scattered and its sums waited for twice: 4096 x 7168 bf16 43.0 us
+// against 36.4, 4096 x 18432 f32 155 against 147.)
 #include "host_util.h"
 #include "tile8.h"
 #include "train_launch.h"
@@ -101,19 +104,25 @@ struct Place {
 };
 
 // ------------------------------------------------------------------------------------------------
-// Forward, tiles along the columns. U groups of eight columns a thread, the next row's loaded while this one is worked on.
+// Forward: the statistics, and with TILES the columns' tiles and the output. U groups of eight columns a thread, the next row's
+// loaded while this one is worked on. With TILES a workgroup's rows follow one another, so that the scales it writes (rows
+// contiguous) meet in lines of its own L2; without, rows are dealt in turn, so that the last ones are those that the Infinity
+// Cache still holds when the second kernel begins with them.
+//
+// 4096 x 7168 bf16, columns' tiles: 22 us, 4.1 TB/s (a copy of x takes 21 us); without its loads or its stores 18 to 20, so
+// HBM, sums and quantization overlap and none of them alone bounds it. 4096 x 18432 f32: 85 us, 4.5 TB/s; there HBM does.
 //
 // FEW rows: a thread has as few groups as 16 waves a row allow, and gamma and beta in registers; a call's time is the latency
-// of its loads (one row of 1024: 2.3 us). Many: two groups (three past 16384 columns), so that what a row costs besides its elements (sums,
-// joins) is shared by more of them, and gamma and beta in LDS.
+// of its loads (one row of 1024: 2.3 us). Many: two groups (three past 16384 columns), so that what a row costs besides its elements
+// (sums, joins) is shared by more of them, and gamma and beta in LDS.
 // ------------------------------------------------------------------------------------------------
-template <int U, bool XB, bool LAYER, bool FEW>
+template <int U, bool XB, bool LAYER, bool FEW, bool TILES>
 __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel(FgNorm p, int waves, int64_t rows_each) {
     __shared__ float part[2][kMaxWaves][2];         // a row's waves: sum, and sum of squares about the wave's mean
     extern __shared__ __attribute__((aligned(16))) float weights[];    // gamma, then beta
     const Place at(waves, p.cols);
-    const int64_t row0 = (int64_t)blockIdx.x * rows_each;
-    const int64_t end = row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
+    const int64_t row0 = (int64_t)blockIdx.x * (TILES ? rows_each : at.groups), step = (int64_t)at.groups * (TILES ? 1 : gridDim.x);
+    const int64_t end = TILES && row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
     const float n = (float)p.cols;
 
     Raw8 next[U];
@@ -130,14 +139,14 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
         w.load(from, 8 * c, p.w_bf16);
         w.get(f, p.w_bf16);
     };
-    if constexpr (FEW) {
+    if constexpr (TILES && FEW) {
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (at.past<U>(u)) continue;
             weight(p.gamma, at.t + u * at.span, gamma[u]);
             if (p.beta) weight(p.beta, at.t + u * at.span, beta[u]);
         }
-    } else {
+    } else if constexpr (TILES) {
         for (int c = threadIdx.x; c < at.chunks; c += (int)blockDim.x) {
             weight(p.gamma, c, gamma[0]);
             store8(weights, 8 * c, gamma[0], 0);
@@ -152,12 +161,12 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
 #pragma unroll
     for (int u = 0; u < U; u++) scales[u] = p.s_cols + (int64_t)((at.t + u * at.span) >> 4) * p.rows;
     int parity = 0;
-    for (int64_t base = row0; base < end; base += at.groups, parity ^= 1) {
+    for (int64_t base = row0; base < end; base += step, parity ^= 1) {
         const int64_t row = base + at.group;
         float v[U][8];
 #pragma unroll
         for (int u = 0; u < U; u++) next[u].get(v[u], XB);
-        load(row + at.groups);
+        load(row + step);
 
         float sum = 0.0f, mean = 0.0f, square = 0.0f;
         if constexpr (LAYER) {
@@ -207,6 +216,7 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
             if (LAYER && p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
+        if constexpr (!TILES) continue;
         float top[U], s[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -258,19 +268,19 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
 }
 
 // ------------------------------------------------------------------------------------------------
-// Forward, tiles along the rows: a 512-thread workgroup takes 128 rows x 128 columns and reads x again (from the Infinity
-// Cache where it fits), with the statistics of the kernel above. Thread t holds rows 4 (t / 16) + i of the eight
-// columns t % 16; the columns' maxima and the codes go through LDS.
+// Forward, both tilings and the output: a 512-thread workgroup takes 128 rows x 128 columns and reads x again (from the Infinity
+// Cache where it fits, hence the last rows first), with the statistics of the kernel above. Thread t holds rows 4 (t / 16) + i
+// of the eight columns t % 16: a row's tile is a DPP row, while the columns' maxima and codes go through LDS.
 // ------------------------------------------------------------------------------------------------
 template <bool LAYER>
-__global__ __launch_bounds__(512) void fg_norm_tokens_kernel(FgNorm p) {
+__global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[16384];       // maxima [32][128], then codes [128 columns][128 rows]
     __shared__ float col_s[128], col_r[128];
     __shared__ int small_w[2];
     float* colmax = reinterpret_cast<float*>(smem);
     const int tid = threadIdx.x, lane = tid & 63, chunk = tid & 15, rgrp = tid >> 4;
     const uint32_t blocks = (uint32_t)(p.cols / FG_GROUP);
-    const int64_t g = blockIdx.x % blocks, br = blockIdx.x / blocks;
+    const int64_t g = blockIdx.x % blocks, br = (gridDim.x - 1 - blockIdx.x) / blocks;
     const int64_t r0 = br * FG_GROUP + 4 * rgrp, col = g * FG_GROUP + 8 * chunk;
 
     Raw8 raw[4], w;
@@ -297,7 +307,18 @@ __global__ __launch_bounds__(512) void fg_norm_tokens_kernel(FgNorm p) {
             y[i][e] = p.beta ? __builtin_fmaf(h, gamma[e], beta[e]) : h * gamma[e];
         }
     }
-    float m[8];
+    float top[4], s[4], m[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) top[i] = fg_row16_max(absmax8(y[i]));
+    fg_scales_from_amax(top, p.pow2, s);
+    const bool small = fg_any_small(__builtin_fminf(__builtin_fminf(s[0], s[1]), __builtin_fminf(s[2], s[3])));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint2 q = small ? quant8<true>(y[i], s[i]) : quant8<false>(y[i], s[i]);
+        *reinterpret_cast<uint2*>(p.q_cols + (r0 + i) * p.cols + col) = q;
+        if (p.y) store8(p.y + (r0 + i) * p.cols, (uint32_t)col, y[i], 1);
+    }
+    if (chunk == 0) *reinterpret_cast<float4*>(p.s_cols + g * p.rows + r0) = make_float4(s[0], s[1], s[2], s[3]);
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         m[e] = 0.0f;
@@ -309,16 +330,16 @@ __global__ __launch_bounds__(512) void fg_norm_tokens_kernel(FgNorm p) {
     out[1] = v4f{m[4], m[5], m[6], m[7]};
     __syncthreads();
     if (tid < 128) {
-        float top = 0.0f;
+        float most = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 32; r++) top = __builtin_fmaxf(top, colmax[r * 128 + tid]);
-        const float s = fg_scale_from_amax(top, p.pow2);
-        const fg_divisor d = fg_divisor_of(s);
+        for (int r = 0; r < 32; r++) most = __builtin_fmaxf(most, colmax[r * 128 + tid]);
+        const float scale = fg_scale_from_amax(most, p.pow2);
+        const fg_divisor d = fg_divisor_of(scale);
         col_s[tid] = d.s;
         col_r[tid] = d.r;
-        const bool small = fg_any_small(s);
-        if (lane == 0) small_w[tid >> 6] = small;
-        p.s_rows[br * p.cols + g * FG_GROUP + tid] = s;
+        const bool tiny = fg_any_small(scale);
+        if (lane == 0) small_w[tid >> 6] = tiny;
+        p.s_rows[br * p.cols + g * FG_GROUP + tid] = scale;
     }
     __syncthreads();
     uint8_t* even = smem + chunk * 1024 + ((rgrp >> 2) ^ (chunk & 7)) * 16 + (rgrp & 3) * 4;
@@ -575,11 +596,11 @@ hipError_t by_groups(int64_t cols, Fn&& fn) {
     }
 }
 
-template <int U, bool FEW>
+template <int U, bool FEW, bool TILES>
 hipError_t launch_fwd(const FgNorm& p, int waves, int groups, int64_t fill, hipStream_t stream) {
     const int64_t each = ((p.rows + fill - 1) / fill + groups - 1) / groups * groups;
     const unsigned grid = (unsigned)((p.rows + each - 1) / each), threads = 64u * waves * groups;
-    const int lds = FEW ? 0 : (int)p.cols * (p.beta ? 8 : 4);
+    const int lds = FEW || !TILES ? 0 : (int)p.cols * (p.beta ? 8 : 4);
     auto go = [&](auto kern, std::atomic<uint64_t>& limit_set) {
         if (lds > 0) {
             const hipError_t e = fg_set_lds_limit_once((const void*)kern, (int)kFgNormMaxCols * 8, limit_set);
@@ -589,8 +610,8 @@ hipError_t launch_fwd(const FgNorm& p, int waves, int groups, int64_t fill, hipS
         return hipGetLastError();
     };
     static std::atomic<uint64_t> limits[4];
-    if (p.x_bf16) return p.layer ? go(fg_norm_kernel<U, true, true, FEW>, limits[0]) : go(fg_norm_kernel<U, true, false, FEW>, limits[1]);
-    return p.layer ? go(fg_norm_kernel<U, false, true, FEW>, limits[2]) : go(fg_norm_kernel<U, false, false, FEW>, limits[3]);
+    if (p.x_bf16) return p.layer ? go(fg_norm_kernel<U, true, true, FEW, TILES>, limits[0]) : go(fg_norm_kernel<U, true, false, FEW, TILES>, limits[1]);
+    return p.layer ? go(fg_norm_kernel<U, false, true, FEW, TILES>, limits[2]) : go(fg_norm_kernel<U, false, false, FEW, TILES>, limits[3]);
 }
 
 constexpr int64_t kMaxPartials = 256;
@@ -603,24 +624,28 @@ int bwd_groups(int64_t cols) { return max_waves(groups_of_thread(cols)) / waves_
 }  // namespace
 
 hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
-    const int64_t cus = fg_device_cus(), units = (p.cols + 511) / 512;
-    hipError_t e;
-    if (p.rows <= kFewRows) {
-        const int waves = waves_of_row(p.cols), groups = std::max(1, 4 / waves);
-        e = by_groups(p.cols, [&](auto u) { return launch_fwd<decltype(u)::value, true>(p, waves, groups, cus * (32 / (waves * groups)), stream); });
-    } else {
+    auto rows = [&](auto tiles) {
+        constexpr bool TILES = decltype(tiles)::value;
+        const int64_t cus = fg_device_cus(), units = (p.cols + 511) / 512;
+        if (TILES && p.rows <= kFewRows) {
+            const int waves = waves_of_row(p.cols), groups = std::max(1, 4 / waves);
+            return by_groups(p.cols, [&](auto u) {
+                return launch_fwd<decltype(u)::value, true, true>(p, waves, groups, cus * (32 / (waves * groups)), stream);
+            });
+        }
         const int u = (int)std::min<int64_t>(units, units <= 32 ? 2 : 3), waves = (int)((units + u - 1) / u), groups = std::max(1, 4 / waves);
         const int64_t fill = cus * std::max(1, 16 / (waves * groups));
         switch (u) {
-            case 1: e = launch_fwd<1, false>(p, waves, groups, fill, stream); break;
-            case 2: e = launch_fwd<2, false>(p, waves, groups, fill, stream); break;
-            default: e = launch_fwd<3, false>(p, waves, groups, fill, stream); break;
+            case 1: return launch_fwd<1, false, TILES>(p, waves, groups, fill, stream);
+            case 2: return launch_fwd<2, false, TILES>(p, waves, groups, fill, stream);
+            default: return launch_fwd<3, false, TILES>(p, waves, groups, fill, stream);
         }
-    }
+    };
+    const hipError_t e = p.q_rows ? rows(std::false_type{}) : rows(std::true_type{});
     if (e != hipSuccess || !p.q_rows) return e;
     const unsigned tiles = (unsigned)((p.cols / FG_GROUP) * (p.rows / FG_GROUP));
-    if (p.layer) hipLaunchKernelGGL((fg_norm_tokens_kernel<true>), dim3(tiles), dim3(512), 0, stream, p);
-    else hipLaunchKernelGGL((fg_norm_tokens_kernel<false>), dim3(tiles), dim3(512), 0, stream, p);
+    if (p.layer) hipLaunchKernelGGL((fg_norm_tiles_kernel<true>), dim3(tiles), dim3(512), 0, stream, p);
+    else hipLaunchKernelGGL((fg_norm_tiles_kernel<false>), dim3(tiles), dim3(512), 0, stream, p);
     return hipGetLastError();
 }
 
