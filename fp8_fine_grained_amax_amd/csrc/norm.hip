@@ -365,16 +365,21 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Backward. The threads of a row as in the forward kernel with few rows, and the next row's inputs loaded ahead as there; a
-// workgroup's rows follow one another, and each thread adds up its own columns' dy xhat and dy over them. The groups of a
-// workgroup join in LDS, the workgroups in a second launch.
+// Backward. The threads of a row as in the forward kernel with few rows; a workgroup's rows follow one another, and each thread
+// adds up its own columns' dy xhat and dy over them. The groups of a workgroup join in LDS, the workgroups in a second launch:
+// no atomics, so that the result depends on the sizes only.
+//
+// HBM bounds it: x, dy and the residual's gradient are read once and dx is written (inputs bf16, f32, bf16; dx bf16). Up to
+// 8192 columns the next row is loaded while this one is worked on: 4096 x 7168 58 us, 5.0 TB/s; 16384 x 2048 58 us, 5.7 TB/s
+// (a copy reaches 4.7 to 5.2). With two and three groups a thread the registers do not hold a second row: 4096 x 12288 108 us,
+// 4.7 TB/s, 4096 x 18432 160 us, 4.7 TB/s. 256 x 1024 takes 6.8 us and the sums 2.6: latency of loads, sums and joins.
 // ------------------------------------------------------------------------------------------------
 template <int U, bool LAYER, bool BIAS>
 __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBwd p, int waves, int64_t rows_each, int64_t partials) {
     constexpr bool AHEAD = U == 1;                  // with more groups the registers do not hold a second row
     __shared__ float part[2][kMaxWaves][2];
     constexpr bool HELD = U > 2;                    // the columns' sums are held in LDS, dgamma's and then dbeta's
-    extern __shared__ __attribute__((aligned(16))) float join[];       // else [groups][cols], with more than one group
+    extern __shared__ __attribute__((aligned(16))) float join[];       // else with more than one group [groups][cols] of dgamma's, then dbeta's
     const Place at(waves, p.cols);
     const int64_t row0 = (int64_t)blockIdx.x * rows_each;
     const int64_t end = row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
@@ -440,7 +445,7 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
             load(row, rx, rd);
         }
         const float rstd = next_rstd, mean = next_mean;
-        if constexpr (AHEAD) load(row + at.groups, nx, nd);
+        if constexpr (AHEAD) load(row + at.groups, nx, nd);     // behind the last row it again: a branch costs 58 -> 65 us at 4096 x 7168
         float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -514,24 +519,6 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
         }
     }
     if (!p.partial) return;
-    [[maybe_unused]] auto put = [&](auto& v, float* out) {
-        if (at.groups > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                if (!behind(u)) store8(join, at.group * (uint32_t)p.cols + 8 * (at.t + u * at.span), v[HELD ? 0 : u], 0);
-            __syncthreads();
-            for (int c = threadIdx.x; c < (int)p.cols; c += (int)blockDim.x) {
-                float s = 0.0f;
-                for (int g = 0; g < at.groups; g++) s += join[g * (int)p.cols + c];
-                out[c] = s;
-            }
-        } else {
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                if (!behind(u)) store8(out, 8 * (at.t + u * at.span), v[HELD ? 0 : u], 0);
-        }
-    };
     float *out_g = p.partial + (int64_t)blockIdx.x * p.cols, *out_b = p.partial + (partials + (int64_t)blockIdx.x) * p.cols;
     if constexpr (HELD) {
 #pragma unroll
@@ -543,9 +530,34 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
                 if constexpr (BIAS) *reinterpret_cast<v4f*>(out_b + c + e) = *reinterpret_cast<const v4f*>(join + p.cols + c + e);
             }
         }
+    } else if (at.groups == 1) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = 8 * (at.t + u * at.span);
+            if (behind(u)) continue;
+            if (p.dgamma) store8(out_g, c, dg[u], 0);
+            if constexpr (BIAS) store8(out_b, c, db[u], 0);
+        }
     } else {
-        if (p.dgamma) put(dg, out_g);
-        if constexpr (BIAS) put(db, out_b);
+        const int cols = (int)p.cols;
+        float* join_b = join + at.groups * cols;
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int c = at.group * cols + 8 * (at.t + u * at.span);
+            if (behind(u)) continue;
+            store8(join, c, dg[u], 0);
+            if constexpr (BIAS) store8(join_b, c, db[u], 0);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += (int)blockDim.x) {
+            float s = 0.0f, t = 0.0f;
+            for (int g = 0; g < at.groups; g++) {
+                s += join[g * cols + c];
+                if constexpr (BIAS) t += join_b[g * cols + c];
+            }
+            if (p.dgamma) out_g[c] = s;
+            if constexpr (BIAS) out_b[c] = t;
+        }
     }
 }
 
@@ -664,11 +676,11 @@ hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream) {
         const unsigned threads = 64u * waves * groups;
         // the groups' joins, or past 12288 columns the columns' sums
         const bool held = groups_of_thread(p.cols) > 2;
-        const int bytes = (int)p.cols * 4 * (held ? (p.dbeta ? 2 : 1) : groups > 1 && p.partial ? groups : 0);
+        const int bytes = (int)p.cols * 4 * (p.dbeta ? 2 : 1) * (held ? 1 : groups > 1 && p.partial ? groups : 0);
         const hipError_t e = by_groups(p.cols, [&](auto u) {
             constexpr int U = decltype(u)::value;
             auto go = [&](auto kern, std::atomic<uint64_t>& limit_set) {
-                if (held) {
+                if (bytes > 0) {
                     const hipError_t e = fg_set_lds_limit_once((const void*)kern, (int)kFgNormMaxCols * 8, limit_set);
                     if (e != hipSuccess) return e;
                 }
