@@ -1,9 +1,12 @@
-// Orthogonalised update by Newton-Schulz products (gfx950): A = X X^T, B = b A + c A A, X = a X + B X, a few times over.
+// Orthogonalised update by Newton-Schulz products (gfx950): A = X X^T, B = a I + b A + c A A, X = B X, a few times over.
 //
 // Three products a step, m x m x n, m x m x m and m x n x m with m the smaller side, bound by the matrix cores. Operands
 // are fp16: bf16's 8 bits make an update 1e-2 off, fp16's 11 bits 1.3e-3 (simulated, 768 x 2048), at the same rate, and the
 // range suffices, since |X| <= 1 at the start and the steps keep its singular values below about 1.2. X is held times
 // 2^12, whose entries of a large matrix would be denormal otherwise (1e-4), A and B times 2^11 (|B| stays below 30).
+// With a I inside B, a and B's diagonal share a rounding; a X beside B X instead is a little less exact where gradients have many
+// independent tokens (simulated: 512 x 512 1.31e-3 against 1.23e-3, 256 x 1024 1.47e-3 and 1.09e-3) and more where X X^T is
+// diagonal (1.5e-3 and 2.0e-3), and reading X once more at every tile's end took 14 us a round of 256 x 256 tiles.
 //
 // Every product is one of rows with rows (C[i][j] = sum_k P[i][k] Q[j][k]): X X^T and A A (A is symmetric) as they are, B X
 // from a transposed copy of X that the last product wrote beside X itself. The symmetric ones compute the tiles on and
@@ -28,17 +31,21 @@ constexpr int kNormParts = 256;                  // partial sums of a matrix's s
 int64_t pad(int64_t v) { return (v + BK - 1) / BK * BK; }
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// C = alpha P Q^T + beta E of every matrix of a batch; E and C have the same shape.
+// A step's products. A and B are symmetric: out and out_t are the same matrix. The last X leaves as bf16 without padding; the
+// others are fp16 with zeros up to their strides. Each has kernels of its own: a small product's time is mostly that of code
+// that runs once, and a kernel for all of them has twice as much of it.
+enum Product { PRODUCT_A, PRODUCT_B, PRODUCT_X, PRODUCT_LAST };
+constexpr bool symmetric(Product P) { return P == PRODUCT_A || P == PRODUCT_B; }
+
+// C = alpha P Q^T of every matrix of a batch; in B beta E + diag I beside it, E of the same shape.
 struct OrthoGemm {
-    const uint16_t *p, *q, *e;                   // fp16 [M][ld], [N][ld], [M][ld_e] or NULL
-    uint16_t *out, *out_t;                       // [M][ld_out], [N][ld_t], either may be NULL: 16 bits an element
+    const uint16_t *p, *q, *e;                   // fp16 [M][ld], [N][ld], [M][ld_e]
+    uint16_t *out, *out_t;                       // [M][ld_out], [N][ld_t], either may be NULL
     int64_t p_batch, q_batch, e_batch, out_batch, t_batch;
     int64_t ld, ld_e, ld_out, ld_t;
     int M, N, batch;
-    float alpha, beta;
-    int symmetric;                               // out and out_t are the same matrix
+    float alpha, beta, diag;
     int first, count;                            // the 256 x 256 tiles to compute, on tiles of 128 in quarters; count 0: everything
-    int bf16;                                    // outputs are bf16 without padding; fp16 with zeros up to their strides if not
 };
 
 __device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -81,11 +88,12 @@ __device__ __forceinline__ void triangle(int id, int& i, int& j) {
 __device__ __forceinline__ int frag_at(int row, int c) { return row * 128 + ((c ^ swz128(row)) << 4); }
 
 // The 256 x 256 tile number id of a batch.
+template <Product P>
 __device__ __forceinline__ void big_tile(const OrthoGemm& p, int id, int64_t& batch, int& ti, int& tj) {
     const int m_tiles = (p.M + 255) / 256, n_tiles = (p.N + 255) / 256;
-    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles, local = id % per;
+    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles, local = id % per;
     batch = id / per;
-    if (p.symmetric) {
+    if constexpr (symmetric(P)) {
         triangle(local, ti, tj);
     } else {
         constexpr int GM = 8;                            // rows of tiles that an XCD's run goes down together
@@ -100,44 +108,40 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
-__device__ __forceinline__ uint32_t half_bits(float v, int bf16) {
-    return bf16 ? (uint32_t)__builtin_bit_cast(unsigned short, (__bf16)v) : (uint32_t)__builtin_bit_cast(unsigned short, (_Float16)v);
-}
+template <class T>
+__device__ __forceinline__ uint32_t half_bits(float v) { return (uint32_t)__builtin_bit_cast(unsigned short, (T)v); }
 
-// E's elements of a wave's 16 x 16 tiles, four to a lane, loaded together (in bounds); zeros without E. (wr, wc): the wave's first
-// row and column in the workgroup's tile.
-template <int MSUB, int NSUB>
+// E's elements of a wave's 16 x 16 tiles, four to a lane, loaded together (in bounds). (wr, wc): the wave's first row and column
+// in the workgroup's tile.
+template <Product P, int MSUB, int NSUB>
 __device__ __forceinline__ void load_e(const OrthoGemm& p, uint2 (&w)[MSUB][NSUB], int64_t batch, int m0, int n0, int wr, int wc) {
-    if (p.e) {
-        const int lane = threadIdx.x & 63;
-        const uint16_t* e = p.e + batch * p.e_batch + (int64_t)m0 * p.ld_e;
+    if constexpr (P != PRODUCT_B) return;
+    const int lane = threadIdx.x & 63;
+    const uint16_t* e = p.e + batch * p.e_batch + (int64_t)m0 * p.ld_e;
 #pragma unroll
-        for (int i = 0; i < MSUB; i++) {
-            const int r = wr + 16 * i + (lane & 15);
-            const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld_e;
+    for (int i = 0; i < MSUB; i++) {
+        const int r = wr + 16 * i + (lane & 15);
+        const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld_e;
 #pragma unroll
-            for (int j = 0; j < NSUB; j++) {
-                const int n = n0 + wc + 16 * j + 4 * (lane >> 4);
-                w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld_e ? n : 0)));
-            }
+        for (int j = 0; j < NSUB; j++) {
+            const int n = n0 + wc + 16 * j + 4 * (lane >> 4);
+            w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld_e ? n : 0)));
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < MSUB; i++)
-#pragma unroll
-            for (int j = 0; j < NSUB; j++) w[i][j] = make_uint2(0, 0);
     }
 }
 
-// The end of a workgroup's tile: alpha acc + beta E, stored in rows and, turned, in columns. Lane l holds row l % 16 and columns
+// The end of a workgroup's tile (`diagonal`: of a symmetric product, on the diagonal): alpha acc and what B adds, stored in rows and, turned, in columns. Lane l holds row l % 16 and columns
 // 4 (l / 16) .. + 3 of every 16 x 16 tile. The finished tile goes through an LDS image [BM rows][BN / 8 chunks of 8], chunk c
 // of row r at c ^ (r % 16) (% 8 with 64 columns), which is read in rows, and in columns by the transposing read: 16 lanes
 // read 4 rows x 16 columns, four columns a lane, and each gets one column's four rows.
-template <int BM, int BN, int THREADS, int MSUB, int NSUB>
+template <Product P, int BM, int BN, int THREADS, int MSUB, int NSUB>
 __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB][NSUB], const uint2 (&w)[MSUB][NSUB], uint8_t* smem,
                                        int64_t batch, int m0, int n0, int wr, int wc, bool diagonal) {
     constexpr int MIX = BN / 8 < 16 ? BN / 8 - 1 : 15;
+    constexpr bool LAST = P == PRODUCT_LAST;
+    using T = std::conditional_t<LAST, __bf16, _Float16>;
     const int tid = threadIdx.x, lane = tid & 63, lrow = lane & 15, g16 = lane >> 4;
+    [[maybe_unused]] const float diag = diagonal ? p.diag : 0.0f;
 #pragma unroll
     for (int i = 0; i < MSUB; i++) {
         const int r = wr + 16 * i + lrow, m = m0 + r;
@@ -147,19 +151,22 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; k++) {
-                const uint32_t h = k & 2 ? w[i][j].y : w[i][j].x;
-                const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
-                v[k] = __builtin_fmaf(p.beta, old, p.alpha * acc[i][j][k]);
-                if (m >= p.M || n + k >= p.N) v[k] = 0.0f;      // padding
+                v[k] = p.alpha * acc[i][j][k];
+                if constexpr (P == PRODUCT_B) {
+                    const uint32_t h = k & 2 ? w[i][j].y : w[i][j].x;
+                    const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
+                    v[k] = __builtin_fmaf(p.beta, old, v[k]) + (m == n + k ? diag : 0.0f);
+                }
+                if (!LAST && (m >= p.M || n + k >= p.N)) v[k] = 0.0f;      // padding
             }
             *reinterpret_cast<uint2*>(smem + r * (2 * BN) + (((c >> 3) ^ (r & MIX)) << 4) + ((c >> 2) & 1) * 8) =
-                make_uint2(half_bits(v[0], p.bf16) | (half_bits(v[1], p.bf16) << 16), half_bits(v[2], p.bf16) | (half_bits(v[3], p.bf16) << 16));
+                make_uint2(half_bits<T>(v[0]) | (half_bits<T>(v[1]) << 16), half_bits<T>(v[2]) | (half_bits<T>(v[3]) << 16));
         }
     }
     __syncthreads();
     // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
     auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
-        if (p.bf16 && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
+        if (LAST && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
             const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 8; k++)
@@ -171,7 +178,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
     if (p.out) {
         constexpr int CH = BN / 8;
         uint16_t* out = p.out + batch * p.out_batch;
-        const int width = p.bf16 ? p.N : (int)p.ld_out;
+        const int width = LAST ? p.N : (int)p.ld_out;
 #pragma unroll 4
         for (int it = 0; it < BM * CH / THREADS; it++) {
             const int f = it * THREADS + tid, r = f / CH, c = f % CH;
@@ -182,7 +189,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
     if (p.out_t && !diagonal) {
         constexpr int CH = BM / 8;
         uint16_t* out = p.out_t + batch * p.t_batch;
-        const int width = p.bf16 ? p.M : (int)p.ld_t;
+        const int width = LAST ? p.M : (int)p.ld_t;
 #pragma unroll 4
         for (int it = 0; it < BN * CH / THREADS; it++) {
             const int f = it * THREADS + tid, c0 = f / (16 * CH) * 16, r = 8 * (f / 16 % CH), col = c0 + 4 * (lrow & 3);     // column c0 + lrow, rows r .. r + 7
@@ -205,26 +212,26 @@ struct MidTile {
     static constexpr int NTHREADS = 256, BM = 128, BN = 128, SUB = 4, STAGE = (BM + BN) * 128, LOADS = 8;
 };
 
-template <int STAGES>
+template <Product P, int STAGES>
 __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_kernel(OrthoGemm p) {
     using C = MidTile;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
-    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
+    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
     int ti, tj;
     int64_t batch;
     if (p.count) {                                       // quarters of 256 x 256 tiles
         const int id = xcd_remap((int)blockIdx.x, 4 * p.count);
-        big_tile(p, p.first + (id >> 2), batch, ti, tj);
+        big_tile<P>(p, p.first + (id >> 2), batch, ti, tj);
         ti = 2 * ti + (id >> 1 & 1);
         tj = 2 * tj + (id & 1);
-        if (ti >= m_tiles || tj >= n_tiles || (p.symmetric && tj > ti)) return;
+        if (ti >= m_tiles || tj >= n_tiles || (symmetric(P) && tj > ti)) return;
     } else {
         const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
         batch = id / per;
-        if (p.symmetric) triangle(local, ti, tj);
+        if constexpr (symmetric(P)) triangle(local, ti, tj);
         else ti = local % m_tiles, tj = local / m_tiles;
     }
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
@@ -270,7 +277,7 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
         for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
     uint2 e[C::SUB][C::SUB];
-    load_e(p, e, batch, m0, n0, wm * 64, wn * 64);
+    load_e<P>(p, e, batch, m0, n0, wm * 64, wn * 64);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < STAGES; s++) issue(s, s);
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();                                    // the stages are free
 
-    finish<C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 64, wn * 64, p.symmetric && ti == tj);
+    finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 64, wn * 64, symmetric(P) && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -331,6 +338,7 @@ struct BigTile {
     static constexpr int NTHREADS = 512, BM = 256, BN = 256, MSUB = 8, NSUB = 4, STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
 };
 
+template <Product P>
 __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(OrthoGemm p) {
     using C = BigTile;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -338,7 +346,7 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     const int wm = wave >> 2, wn = wave & 3;
     int64_t batch;
     int ti, tj;
-    big_tile(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
+    big_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
     const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
     const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
@@ -436,8 +444,8 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();                                     // the stages are free
     uint2 e[C::MSUB][C::NSUB];
-    load_e(p, e, batch, m0, n0, wm * 128, wn * 64);
-    finish<C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 128, wn * 64, p.symmetric && ti == tj);
+    load_e<P>(p, e, batch, m0, n0, wm * 128, wn * 64);
+    finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 128, wn * 64, symmetric(P) && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -453,17 +461,17 @@ struct SmallTile {
     static constexpr int LDS = SLOTS == 2 ? WAVES * 2 * STAGE : WAVES * STAGE + 8192;
 };
 
-template <int SLOTS>
+template <Product P, int SLOTS>
 __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGemm p) {
     using C = SmallTile<SLOTS>;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m_tiles = (p.M + C::SIDE - 1) / C::SIDE, n_tiles = (p.N + C::SIDE - 1) / C::SIDE;
-    const int per = p.symmetric ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
+    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
     const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
     const int64_t batch = id / per;
     int ti, tj;
-    if (p.symmetric) triangle(local, ti, tj);
+    if constexpr (symmetric(P)) triangle(local, ti, tj);
     else ti = local % m_tiles, tj = local / m_tiles;
     const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = (int)(p.ld / BK);
     const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
@@ -496,7 +504,7 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 #pragma unroll
         for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     uint2 e[1][C::SUB];                                  // of the strip of 16 rows that the wave ends with
-    load_e(p, e, batch, m0, n0, 16 * wave, 0);
+    load_e<P>(p, e, batch, m0, n0, 16 * wave, 0);
     __builtin_amdgcn_sched_barrier(0);
     issue(wave, 0);
     if constexpr (SLOTS == 2) issue(wave + C::WAVES, 1);
@@ -539,7 +547,7 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 #pragma unroll
         for (int w = 1; w < C::WAVES; w++) sum[0][j] += red[((w * C::SUB + wave) * C::SUB + j) * 64 + lane];
     }
-    finish<C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, p.symmetric && ti == tj);
+    finish<P, C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, symmetric(P) && ti == tj);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -633,7 +641,7 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const bool there = r0 + r + k < p.N && c0 + c + j < p.K;     // a factor of NaN leaves the padding 0
-            h[k][j] = there ? half_bits(v[k][j] * inv * kScaleX, 0) : 0;
+            h[k][j] = there ? half_bits<_Float16>(v[k][j] * inv * kScaleX) : 0;
         }
 #pragma unroll
     for (int k = 0; k < 4; k++) {
@@ -657,31 +665,34 @@ hipError_t launch(Kernel kern, int64_t tiles, int lds, std::atomic<uint64_t>& li
     return hipGetLastError();
 }
 
+template <Product P>
 hipError_t launch_tile(OrthoTile tile, const OrthoGemm& p, hipStream_t stream) {
     static std::atomic<uint64_t> limits[5];
-    auto tiles = [&](int side) { return ortho_tiles(p.batch, p.M, p.N, p.symmetric, side); };
+    auto tiles = [&](int side) { return ortho_tiles(p.batch, p.M, p.N, symmetric(P), side); };
     const int64_t quarters = p.count ? 4 * (int64_t)p.count : tiles(128);
     switch (tile) {
         case TILE_64:
-            if (tiles(64) <= fg_device_cus()) return launch<SmallTile<2>>(fg_ortho_small_kernel<2>, tiles(64), SmallTile<2>::LDS, limits[0], p, stream);
-            return launch<SmallTile<1>>(fg_ortho_small_kernel<1>, tiles(64), SmallTile<1>::LDS, limits[4], p, stream);
-        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<4>, quarters, 4 * MidTile::STAGE, limits[1], p, stream);
-        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<2>, quarters, 2 * MidTile::STAGE, limits[2], p, stream);
-        default: return launch<BigTile>(fg_ortho_big_kernel, p.count ? p.count : tiles(256), BigTile::LDS, limits[3], p, stream);
+            if (tiles(64) <= fg_device_cus())
+                return launch<SmallTile<2>>(fg_ortho_small_kernel<P, 2>, tiles(64), SmallTile<2>::LDS, limits[0], p, stream);
+            return launch<SmallTile<1>>(fg_ortho_small_kernel<P, 1>, tiles(64), SmallTile<1>::LDS, limits[1], p, stream);
+        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<P, 4>, quarters, 4 * MidTile::STAGE, limits[2], p, stream);
+        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<P, 2>, quarters, 2 * MidTile::STAGE, limits[3], p, stream);
+        default: return launch<BigTile>(fg_ortho_big_kernel<P>, p.count ? p.count : tiles(256), BigTile::LDS, limits[4], p, stream);
     }
 }
 
+template <Product P>
 hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
     const int64_t cus = fg_device_cus();
-    const OrthoTile tile = ortho_tile(p.batch, p.M, p.N, p.symmetric, p.ld / BK, cus);
-    if (tile != TILE_256_TAIL) return launch_tile(tile, p, stream);
-    const int64_t all = ortho_tiles(p.batch, p.M, p.N, p.symmetric, 256), rest = all % cus;
+    const OrthoTile tile = ortho_tile(p.batch, p.M, p.N, symmetric(P), p.ld / BK, cus);
+    if (tile != TILE_256_TAIL) return launch_tile<P>(tile, p, stream);
+    const int64_t all = ortho_tiles(p.batch, p.M, p.N, symmetric(P), 256), rest = all % cus;
     OrthoGemm part = p;
     part.count = (int)(all - rest);
-    if (const hipError_t e = launch_tile(TILE_256, part, stream); e != hipSuccess) return e;
+    if (const hipError_t e = launch_tile<P>(TILE_256, part, stream); e != hipSuccess) return e;
     part.first = part.count;
     part.count = (int)rest;
-    return launch_tile(ortho_tail_tile(rest, cus), part, stream);
+    return launch_tile<P>(ortho_tail_tile(rest, cus), part, stream);
 }
 
 // The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.
@@ -727,27 +738,24 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
         g.p = g.q = x; g.ld = l.np; g.p_batch = g.q_batch = l.m * l.np;
         g.out = g.out_t = a; g.ld_out = g.ld_t = l.mp; g.out_batch = g.t_batch = l.m * l.mp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
-        g.symmetric = 1;
-        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
+        if (const hipError_t e = launch_gemm<PRODUCT_A>(g, stream); e != hipSuccess) return e;
         g.p = g.q = g.e = a; g.ld = g.ld_e = l.mp; g.p_batch = g.q_batch = g.e_batch = l.m * l.mp;
         g.out = g.out_t = b;
-        g.alpha = o.c / kScaleA; g.beta = o.b;
-        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
+        g.alpha = o.c / kScaleA; g.beta = o.b; g.diag = o.a * kScaleA;
+        if (const hipError_t e = launch_gemm<PRODUCT_B>(g, stream); e != hipSuccess) return e;
         g.p = b; g.q = t; g.q_batch = l.n * l.mp; g.N = (int)l.n;
-        g.e = x; g.ld_e = l.np; g.e_batch = l.m * l.np;
-        g.symmetric = 0;
         if (s + 1 < o.steps) {
             g.out = x; g.ld_out = l.np; g.out_batch = l.m * l.np;
             g.out_t = t_next; g.ld_t = l.mp; g.t_batch = l.n * l.mp;
-            g.alpha = 1.0f / kScaleA; g.beta = o.a;
+            g.alpha = 1.0f / kScaleA;
+            if (const hipError_t e = launch_gemm<PRODUCT_X>(g, stream); e != hipSuccess) return e;
         } else {
             g.out = wide ? o.out : nullptr;
             g.out_t = wide ? nullptr : o.out;
             g.ld_out = g.ld_t = o.K; g.out_batch = g.t_batch = o.N * o.K;
-            g.alpha = o.scale / (kScaleA * kScaleX); g.beta = o.a * o.scale / kScaleX;
-            g.bf16 = 1;
+            g.alpha = o.scale / (kScaleA * kScaleX);
+            if (const hipError_t e = launch_gemm<PRODUCT_LAST>(g, stream); e != hipSuccess) return e;
         }
-        if (const hipError_t e = launch_gemm(g, stream); e != hipSuccess) return e;
         std::swap(t, t_next);
     }
     return hipSuccess;

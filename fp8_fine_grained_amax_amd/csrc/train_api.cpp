@@ -43,11 +43,11 @@ double largest(double a, double b, double c, double u) {
     return most;
 }
 
-// Whether the steps keep every product inside fp16's range: |X| below u, |A| below u^2, |B| below |b| u^2 + |c| u^4.
+// Whether the steps keep every product inside fp16's range: |X| below u, |A| below u^2, |B| below |a| + |b| u^2 + |c| u^4.
 bool in_range(double a, double b, double c, int steps) {
     double u = 1.0;
     for (int s = 0; s < steps; s++) {
-        if (!(std::fabs(b) * u * u + std::fabs(c) * u * u * u * u < 30.0)) return false;
+        if (!(std::fabs(a) + std::fabs(b) * u * u + std::fabs(c) * u * u * u * u < 30.0)) return false;
         u = std::max(u, largest(a, b, c, u));
         if (!(u < 5.0)) return false;
     }

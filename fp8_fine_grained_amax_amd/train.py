@@ -74,6 +74,6 @@ def fg_norm_bwd(x, mean, rstd, gamma, dy, residual_grad=None, kind: int = FG_NOR
 def fg_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0, out=None,
                      workspace=None):
     """Orthogonalised update by Newton-Schulz products: of each matrix of g (f32 or bf16, [N, K] or [batch, N, K]), X = g / (|g| +
-    eps), `steps` times X = a X + (b A + c A A) X with A = X X^T, and scale X as bf16."""
+    eps), `steps` times X = (a I + b A + c A A) X with A = X X^T, and scale X as bf16."""
     a, b, c = coefficients
     return _ffn().orthogonalize(g, steps, a, b, c, eps, scale, out, workspace)

@@ -66,7 +66,7 @@ fg_status fg_norm_bwd(const void* x, fg_out_dtype x_type, int64_t ld_x, const fl
 
 /* Orthogonalised update of a weight by Newton-Schulz products (the Muon optimiser's): for each of `batch` matrices
  *   X = G / (|G| + eps), |G| the Frobenius norm,
- *   `steps` times: A = X X^T (X^T X where N > K), B = b A + c A A, X = a X + B X (a X + X B),
+ *   `steps` times: A = X X^T (X^T X where N > K), B = a I + b A + c A A, X = B X (X B),
  *   out = scale X.
  *   g    [batch][N][K] of type g_type, row stride ld_g, matrices N ld_g elements apart: the gradient or momentum.
  *   out  bf16 [batch][N][K].
@@ -75,8 +75,8 @@ fg_status fg_norm_bwd(const void* x, fg_out_dtype x_type, int64_t ld_x, const fl
  *   few directions (rank r) is off by about 0.15 / sqrt(r): the steps raise the rounding in its empty directions, as they
  *   raise small directions.
  *   The coefficients have to keep the iteration inside fp16's range: with u0 = 1 and u the largest |a s + b s^3 + c s^5| for
- *   0 <= s <= u (or u itself, if that is larger), every u stays below 5 and |b| u^2 + |c| u^4 below 30 (FG_ERR_INVALID_ARG otherwise). (3.4445, -4.7750,
- *   2.0315) does, for any steps.
+ *   0 <= s <= u (or u itself, if that is larger), every u stays below 5 and |a| + |b| u^2 + |c| u^4
+ *   below 30 (FG_ERR_INVALID_ARG otherwise). (3.4445, -4.7750, 2.0315) does, for any steps.
  *   A matrix of zeros gives zeros; one that holds a NaN or an infinity, or whose norm overflows fp32, gives NaN.
  *   workspace  fg_orthogonalize_workspace(batch, N, K) bytes, 256-byte aligned; 0 for sizes that are refused here.
  *   N and K at most 65536, batch at most 65535, batch * ceil(N / 64) * ceil(K / 64) < 2^24, 1 <= steps <= 32, a, b, c, eps and scale finite, eps >

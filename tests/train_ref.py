@@ -59,8 +59,8 @@ def largest_singular(gram):
 def orthogonalize(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7, scale=1.0):
     """(update, bound of the fp16 roundings in the 2-norm) of one float64 matrix. To first order a step p(X) = a X + b X X^T X + c
     (X X^T)^2 X takes a change of X to one no larger than the largest |p'| on [0, u] times it, u its largest singular value; a
-    step's own roundings (half a step, 2^-11 relative, of X, A and B) enter it as 2^-11 (L |X| + (|b| |A| + 2 |c| |A| u^2 + |B|)
-    u)."""
+    step's own roundings (half a step, 2^-11 relative, of X, A and B = a I + b A + c A A) enter it as 2^-11 (L |X| + (|b| |A|
+    + 2 |c| |A| u^2 + |B|) u)."""
     a, b, c = coefficients
     x = g if g.shape[0] <= g.shape[1] else g.t()
     x = x / (torch.linalg.matrix_norm(x) + eps)
@@ -71,9 +71,10 @@ def orthogonalize(g, steps=5, coefficients=COEFFICIENTS, eps=1e-7, scale=1.0):
         s = torch.linspace(0, u, 1001, dtype=torch.float64)
         slope = float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max())
         q = b * p + c * (p @ p)
+        q.diagonal().add_(a)
         fro = [float(torch.linalg.matrix_norm(v)) for v in (x, p, q)]
         err = slope * err + half * (slope * fro[0] + (abs(b) * fro[1] + 2 * abs(c) * fro[1] * u * u + fro[2]) * u)
-        x = a * x + q @ x
+        x = q @ x
     x = x if g.shape[0] <= g.shape[1] else x.t()
     return scale * x, abs(scale) * err
 
