@@ -8,9 +8,11 @@
 // independent tokens (simulated: 512 x 512 1.31e-3 against 1.23e-3, 256 x 1024 1.47e-3 and 1.09e-3) and more where X X^T is
 // diagonal (1.5e-3 and 2.0e-3), and reading X once more at every tile's end took 14 us a round of 256 x 256 tiles.
 //
-// Every product is one of rows with rows (C[i][j] = sum_k P[i][k] Q[j][k]): X X^T and A A (A is symmetric) as they are, B X
-// from a transposed copy of X that the last product wrote beside X itself. The symmetric ones compute the tiles on and
-// below the diagonal and write each one twice. Contractions are padded with zeros to multiples of 64.
+// X X^T and A A (A is symmetric) are products of rows with rows (C[i][j] = sum_k P[i][k] Q[j][k]); they compute the tiles on and
+// below the diagonal and write each one twice. B X takes X as it lies: the transposing LDS read turns it on its way into the
+// registers, at the same number of bytes a cycle. (From a transposed copy of X, which every product wrote beside
+// X itself: 8 x 2048 x 7168 4.02 ms against 3.85, 7168 x 18432 12.67 and 12.44, 512 x 1024 by 8 155 us and 144.)
+// Contractions are padded with zeros to multiples of 64.
 #include "host_util.h"
 #include "ortho_shape.h"
 #include "train_launch.h"
@@ -39,10 +41,10 @@ constexpr bool symmetric(Product P) { return P == PRODUCT_A || P == PRODUCT_B; }
 
 // C = alpha P Q^T of every matrix of a batch; in B beta E + diag I beside it, E of the same shape.
 struct OrthoGemm {
-    const uint16_t *p, *q, *e;                   // fp16 [M][ld], [N][ld], [M][ld_e]
-    uint16_t *out, *out_t;                       // [M][ld_out], [N][ld_t], either may be NULL
+    const uint16_t *p, *q, *e;                   // fp16 [M][ld], of A and B [N][ld], of X [ld][ld_q], [M][ld_e]
+    uint16_t *out, *out_t;                       // [M][ld_out] and, of A and B the same, [N][ld_t]; X has the first only, the last one either
     int64_t p_batch, q_batch, e_batch, out_batch, t_batch;
-    int64_t ld, ld_e, ld_out, ld_t;
+    int64_t ld, ld_q, ld_e, ld_out, ld_t;
     int M, N, batch;
     float alpha, beta, diag;
     int first, count;                            // the 256 x 256 tiles to compute, on tiles of 128 in quarters; count 0: everything
@@ -64,7 +66,8 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* lds,
 }
 
 typedef short v4s __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ v2i tr_read(const uint8_t* lds) {
+// The transposing read. (restrict: without it the compiler waits for all loads to LDS before each.)
+__device__ __forceinline__ v2i tr_read(const uint8_t* __restrict__ lds) {
     return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)lds));
 }
 
@@ -86,6 +89,48 @@ __device__ __forceinline__ void triangle(int id, int& i, int& j) {
 // them in lane l: the chunks 2 (l / 16) in one operand and 2 (l / 16) + 1 in the other, for both sides alike. (The order of a
 // contraction is free. With l / 16 and l / 16 + 4 every read had a two-way bank conflict, 5% of the time.)
 __device__ __forceinline__ int frag_at(int row, int c) { return row * 128 + ((c ^ swz128(row)) << 4); }
+
+// The second operand as it lies in X: a stage holds 64 rows (of the contraction) of BN columns, with the pairs of 16-byte chunks
+// XORed with bits of the row, so that the eight rows that 32 lanes read at once lie in different banks: the rows 4 i .. + 3 and
+// those 16 further on.
+template <int BN>
+__device__ __forceinline__ int turn_pair(int k) { return BN == 64 ? (k >> 1 & 1) | (k >> 4 & 1) << 1 : (k & 3) | (k >> 4 & 1) << 2; }
+
+// Byte of the second operand that a lane loads for the 1024 bytes number f of a stage, from the tile's first row or column in the
+// K step on; past the end the last again.
+template <Product P, int BN>
+__device__ __forceinline__ uint32_t q_offset(const OrthoGemm& p, int n0, int f, int lane) {
+    if constexpr (symmetric(P)) {
+        const int row = f * 8 + (lane >> 3), r = n0 + row < p.N ? row : p.N - 1 - n0;
+        return (uint32_t)r * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(row)) << 4);
+    } else {
+        constexpr int CH = BN / 8;
+        const int row = f * (64 / CH) + lane / CH, c = 8 * ((lane % CH) ^ (2 * turn_pair<BN>(row))), last = (int)p.ld_q - 8 - n0;
+        return (uint32_t)row * (uint32_t)(p.ld_q * 2) + 2 * (uint32_t)(c < last ? c : last);
+    }
+}
+// The tile's part of the second operand, and the bytes from a K step of it to the next.
+template <Product P>
+__device__ __forceinline__ const uint8_t* q_first(const OrthoGemm& p, int64_t batch, int n0) {
+    return (const uint8_t*)(p.q + batch * p.q_batch + (symmetric(P) ? (int64_t)n0 * p.ld : n0));
+}
+template <Product P>
+__device__ __forceinline__ int64_t q_step(const OrthoGemm& p) { return symmetric(P) ? 2 * BK : 2 * BK * p.ld_q; }
+
+// Where a lane finds the operand of 16 columns, first / 16 + j of the tile, in a stage, and the operand's eight values of half h.
+template <Product P, int BN>
+__device__ __forceinline__ int q_at(int first, int j, int lane) {
+    const int lrow = lane & 15, g16 = lane >> 4;
+    if constexpr (symmetric(P)) return (first + 16 * j) * 128 + frag_at(lrow, 2 * g16);
+    const int k = 16 * g16 + (lrow >> 2);
+    return k * (2 * BN) + ((((first / 16 + j) ^ turn_pair<BN>(k)) * 2 + (lrow >> 1 & 1)) << 4) + (lrow & 1) * 8;
+}
+template <Product P, int BN>
+__device__ __forceinline__ v8h read_q(const uint8_t* st, int at, int h) {
+    if constexpr (symmetric(P)) return *reinterpret_cast<const v8h*>(st + (at ^ (h << 4)));
+    const v2i a = tr_read(st + at + h * 8 * (2 * BN)), b = tr_read(st + at + (h * 8 + 4) * (2 * BN));
+    return __builtin_bit_cast(v8h, v4i{a.x, a.y, b.x, b.y});
+}
 
 // The 256 x 256 tile number id of a batch.
 template <Product P>
@@ -175,7 +220,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
             *reinterpret_cast<uint4*>(row + c) = v;
         }
     };
-    if (p.out) {
+    if (P != PRODUCT_LAST || p.out) {
         constexpr int CH = BN / 8;
         uint16_t* out = p.out + batch * p.out_batch;
         const int width = LAST ? p.N : (int)p.ld_out;
@@ -186,7 +231,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
                 store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & MIX)) << 4)));
         }
     }
-    if (p.out_t && !diagonal) {
+    if (P != PRODUCT_X && p.out_t && !diagonal) {
         constexpr int CH = BM / 8;
         uint16_t* out = p.out_t + batch * p.t_batch;
         const int width = LAST ? p.M : (int)p.ld_t;
@@ -235,22 +280,19 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
         else ti = local % m_tiles, tj = local / m_tiles;
     }
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
-    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
-    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
 
     uint32_t a_off[4], b_off[4];
 #pragma unroll
     for (int u = 0; u < 4; u++) {
-        const int row = (wave + 4 * u) * 8 + (lane >> 3);
-        const int rm = m0 + row < p.M ? row : p.M - 1 - m0, rn = n0 + row < p.N ? row : p.N - 1 - n0;    // past the end: the last again
-        const uint32_t chunk = ((lane & 7) ^ swz128(row)) << 4;
-        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + chunk;
-        b_off[u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + chunk;
+        const int row = (wave + 4 * u) * 8 + (lane >> 3), rm = m0 + row < p.M ? row : p.M - 1 - m0;    // past the end: the last again
+        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(row)) << 4);
+        b_off[u] = q_offset<P, C::BN>(p, n0, wave + 4 * u, lane);
     }
     auto issue = [&](int kb, int slot) {
         const int k = kb < nkb ? kb : nkb - 1;
         uint8_t* st = smem + slot * C::STAGE;
-        const auto ra = buffer_rsrc(pp + (int64_t)k * 128), rb = buffer_rsrc(qp + (int64_t)k * 128);
+        const auto ra = buffer_rsrc(pp + (int64_t)k * 128), rb = buffer_rsrc(qp + k * q_step<P>(p));
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             load_lds16(ra, st + (wave + 4 * u) * 1024, a_off[u]);
@@ -259,6 +301,9 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     };
     const int lrow = lane & 15, g16 = lane >> 4;
     const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
+    int q_frag[C::SUB];
+#pragma unroll
+    for (int j = 0; j < C::SUB; j++) q_frag[j] = q_at<P, C::BN>(wn * 64, j, lane);
     v8h af[2][C::SUB][2], bf[2][C::SUB][2];
     auto read = [&](int kb, int set) {
         const uint8_t* st = smem + (kb & (STAGES - 1)) * C::STAGE;
@@ -267,7 +312,7 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 af[set][i][h] = *reinterpret_cast<const v8h*>(st + (wm * 64 + 16 * i) * 128 + frag[h]);
-                bf[set][i][h] = *reinterpret_cast<const v8h*>(st + C::BM * 128 + (wn * 64 + 16 * i) * 128 + frag[h]);
+                bf[set][i][h] = read_q<P, C::BN>(st + C::BM * 128, q_frag[i], h);
             }
     };
     v4f acc[C::SUB][C::SUB];
@@ -303,7 +348,8 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
 #pragma unroll
             for (int h = 0; h < 2; h++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bf[set][j][h], af[set][i][h], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two MFMAs
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read of the next step's operands
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // an LDS read of the next step's operands, of X's two to each
+            if (!symmetric(P) && t % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
     };
     int kb = 0;
@@ -348,22 +394,20 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     int ti, tj;
     big_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
     const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
-    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
-    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
 
-    // Loads: an instruction fills 8 rows of 128 bytes. A0 is rows [0, 64) and [128, 192) of the tile, B0 the first 32 of every 64
-    // columns; a wave loads 16 rows of each half.
+    // Loads: an instruction fills 8 rows of 128 bytes. A0 is rows [0, 64) and [128, 192) of the tile; a wave loads 16 rows of
+    // each half and four parts of B.
     auto a_row = [&](int half, int u) { return (wave >> 2) * 128 + half * 64 + (wave & 3) * 16 + u * 8; };
-    auto b_row = [&](int half, int u) { return (wave >> 1) * 64 + half * 32 + (wave & 1) * 16 + u * 8; };
+    auto b_part = [&](int half, int u) { return (wave >> 1) * 8 + half * 4 + (wave & 1) * 2 + u; };
     uint32_t a_off[2][2], b_off[2][2];
 #pragma unroll
     for (int h = 0; h < 2; h++)
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-            const int ra = a_row(h, u) + (lane >> 3), rb = b_row(h, u) + (lane >> 3);
-            const int rm = m0 + ra < p.M ? ra : p.M - 1 - m0, rn = n0 + rb < p.N ? rb : p.N - 1 - n0;    // past the end: the last again
+            const int ra = a_row(h, u) + (lane >> 3), rm = m0 + ra < p.M ? ra : p.M - 1 - m0;    // past the end: the last again
             a_off[h][u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(ra)) << 4);
-            b_off[h][u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(rb)) << 4);
+            b_off[h][u] = q_offset<P, C::BN>(p, n0, b_part(h, u), lane);
         }
     auto load_a = [&](int kb, int half) {
         const auto rs = buffer_rsrc(pp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
@@ -371,13 +415,16 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
         for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + a_row(half, u) * 128, a_off[half][u]);
     };
     auto load_b = [&](int kb, int half) {
-        const auto rs = buffer_rsrc(qp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
+        const auto rs = buffer_rsrc(qp + (kb < nkb ? kb : nkb - 1) * q_step<P>(p));
 #pragma unroll
-        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + (C::BM + b_row(half, u)) * 128, b_off[half][u]);
+        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + C::BM * 128 + b_part(half, u) * 1024, b_off[half][u]);
     };
 
     const int lrow = lane & 15, g16 = lane >> 4;
     const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
+    int q_frag[C::NSUB];
+#pragma unroll
+    for (int j = 0; j < C::NSUB; j++) q_frag[j] = q_at<P, C::BN>(wn * 64, j, lane);
     v8h af[4][2], bf[C::NSUB][2];                        // a half of A's 16-row operands, and B's
     auto read_a = [&](int kb, int half) {
         const uint8_t* st = smem + (kb & 1) * C::STAGE + (wm * 128 + half * 64) * 128;
@@ -387,11 +434,11 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
             for (int h = 0; h < 2; h++) af[i][h] = *reinterpret_cast<const v8h*>(st + 16 * i * 128 + frag[h]);
     };
     auto read_b = [&](int kb) {
-        const uint8_t* st = smem + (kb & 1) * C::STAGE + (C::BM + wn * 64) * 128;
+        const uint8_t* st = smem + (kb & 1) * C::STAGE + C::BM * 128;
 #pragma unroll
         for (int j = 0; j < C::NSUB; j++)
 #pragma unroll
-            for (int h = 0; h < 2; h++) bf[j][h] = *reinterpret_cast<const v8h*>(st + 16 * j * 128 + frag[h]);
+            for (int h = 0; h < 2; h++) bf[j][h] = read_q<P, C::BN>(st, q_frag[j], h);
     };
     v4f acc[C::MSUB][C::NSUB];
 #pragma unroll
@@ -474,22 +521,19 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
     if constexpr (symmetric(P)) triangle(local, ti, tj);
     else ti = local % m_tiles, tj = local / m_tiles;
     const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = (int)(p.ld / BK);
-    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld);
-    const uint8_t* qp = (const uint8_t*)(p.q + batch * p.q_batch + (int64_t)n0 * p.ld);
+    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
     uint8_t* ring = smem + wave * (SLOTS * C::STAGE);
 
     uint32_t a_off[8], b_off[8];
 #pragma unroll
     for (int u = 0; u < 8; u++) {
-        const int row = u * 8 + (lane >> 3);
-        const int rm = m0 + row < p.M ? row : p.M - 1 - m0, rn = n0 + row < p.N ? row : p.N - 1 - n0;    // past the end: the last again
-        const uint32_t chunk = ((lane & 7) ^ swz128(row)) << 4;
-        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + chunk;
-        b_off[u] = (uint32_t)rn * (uint32_t)(p.ld * 2) + chunk;
+        const int row = u * 8 + (lane >> 3), rm = m0 + row < p.M ? row : p.M - 1 - m0;    // past the end: the last again
+        a_off[u] = (uint32_t)rm * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(row)) << 4);
+        b_off[u] = q_offset<P, C::SIDE>(p, n0, u, lane);
     }
     auto issue = [&](int kb, int slot) {
         if (kb >= nkb) return;
-        const auto ra = buffer_rsrc(pp + (int64_t)kb * 128), rb = buffer_rsrc(qp + (int64_t)kb * 128);
+        const auto ra = buffer_rsrc(pp + (int64_t)kb * 128), rb = buffer_rsrc(qp + kb * q_step<P>(p));
 #pragma unroll
         for (int u = 0; u < 8; u++) {
             load_lds16(ra, ring + slot * C::STAGE + u * 1024, a_off[u]);
@@ -498,6 +542,9 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
     };
     const int lrow = lane & 15, g16 = lane >> 4;
     const int frag[2] = {frag_at(lrow, 2 * g16), frag_at(lrow, 2 * g16 + 1)};
+    int q_frag[C::SUB];
+#pragma unroll
+    for (int j = 0; j < C::SUB; j++) q_frag[j] = q_at<P, C::SIDE>(0, j, lane);
     v4f acc[C::SUB][C::SUB];
 #pragma unroll
     for (int i = 0; i < C::SUB; i++)
@@ -520,7 +567,7 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 af[i][h] = *reinterpret_cast<const v8h*>(st + 16 * i * 128 + frag[h]);
-                bf[i][h] = *reinterpret_cast<const v8h*>(st + C::SIDE * 128 + 16 * i * 128 + frag[h]);
+                bf[i][h] = read_q<P, C::SIDE>(st + C::SIDE * 128, q_frag[i], h);
             }
         __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0): the slot is read
         __builtin_amdgcn_sched_barrier(0);
@@ -551,7 +598,7 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 }
 
 // ------------------------------------------------------------------------------------------------
-// The start: |G|, then X and its transpose.
+// The start: |G|, then X.
 // ------------------------------------------------------------------------------------------------
 // Four neighbouring elements of G from element i on, the first `count` of them; `whole`: all four, aligned to their size.
 __device__ __forceinline__ v4f load_g(const FgOrtho& p, int64_t i, int64_t count, bool whole) {
@@ -615,11 +662,14 @@ __global__ __launch_bounds__(kNormThreads) void fg_ortho_norm_kernel(FgOrtho p, 
     if (threadIdx.x == 0) partial[batch * kNormParts + blockIdx.x] = sum;
 }
 
-// 64 x 64 elements of G to both copies of X, zeros behind the last row and column. A thread takes 4 x 4 of them.
-__global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const double* __restrict__ partial, int parts, uint16_t* same,
-                                                             uint16_t* turned, int64_t ld_same, int64_t ld_turned) {
+// 64 x 64 elements of G to X, turned where the rows are the longer side, zeros behind the last row and column; behind the last row
+// of X the zeros go to the other buffer of X as well, which later steps read and nothing writes there. A thread takes 4 x 4
+// elements. WIDE: X is G as it lies.
+template <bool WIDE>
+__global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const double* __restrict__ partial, int parts, uint16_t* x,
+                                                             uint16_t* other, int64_t rows, int64_t ld) {
     __shared__ double red[4];
-    __shared__ __attribute__((aligned(16))) uint16_t tile[64][72];       // [column][row]
+    __shared__ __attribute__((aligned(16))) uint16_t tile[WIDE ? 1 : 64][72];       // [column][row]
     const int64_t batch = blockIdx.y, tiles = (p.K + 63) / 64;
     const int64_t r0 = (int64_t)(blockIdx.x / tiles) * 64, c0 = (int64_t)(blockIdx.x % tiles) * 64;
     const int c = 4 * (threadIdx.x & 15), r = 4 * (threadIdx.x >> 4);
@@ -633,8 +683,6 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
     const double sum = block_sum<4>((int)threadIdx.x < parts ? partial[batch * kNormParts + threadIdx.x] : 0.0, red);
     const float norm = (float)__builtin_sqrt(sum);
     const float inv = norm < __builtin_inff() ? (float)(1.0 / (double)(norm + p.eps)) : __builtin_nanf("");
-    same += batch * p.N * ld_same;
-    turned += batch * p.K * ld_turned;
     uint32_t h[4][4];
 #pragma unroll
     for (int k = 0; k < 4; k++)
@@ -643,17 +691,25 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
             const bool there = r0 + r + k < p.N && c0 + c + j < p.K;     // a factor of NaN leaves the padding 0
             h[k][j] = there ? half_bits<_Float16>(v[k][j] * inv * kScaleX) : 0;
         }
+    const int64_t m = WIDE ? p.N : p.K;
+    x += batch * rows * ld;
+    other += batch * rows * ld;
+    auto put = [&](int64_t row, int64_t col, uint2 w) {
+        *reinterpret_cast<uint2*>(x + row * ld + col) = w;
+        if (row >= m) *reinterpret_cast<uint2*>(other + row * ld + col) = w;
+    };
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        if (r0 + r + k < p.N)
-            *reinterpret_cast<uint2*>(same + (r0 + r + k) * ld_same + c0 + c) = make_uint2(h[k][0] | (h[k][1] << 16), h[k][2] | (h[k][3] << 16));
-        *reinterpret_cast<uint2*>(&tile[c + k][r]) = make_uint2(h[0][k] | (h[1][k] << 16), h[2][k] | (h[3][k] << 16));
-    }
-    __syncthreads();
+        for (int k = 0; k < 4; k++) put(r0 + r + k, c0 + c, make_uint2(h[k][0] | (h[k][1] << 16), h[k][2] | (h[k][3] << 16)));
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const int col = (threadIdx.x >> 4) + 16 * k, row = 4 * (threadIdx.x & 15);
-        if (c0 + col < p.K) *reinterpret_cast<uint2*>(turned + (c0 + col) * ld_turned + r0 + row) = *reinterpret_cast<const uint2*>(&tile[col][row]);
+        for (int k = 0; k < 4; k++) *reinterpret_cast<uint2*>(&tile[c + k][r]) = make_uint2(h[0][k] | (h[1][k] << 16), h[2][k] | (h[3][k] << 16));
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int col = (threadIdx.x >> 4) + 16 * k, row = 4 * (threadIdx.x & 15);
+            put(c0 + col, r0 + row, *reinterpret_cast<const uint2*>(&tile[col][row]));
+        }
     }
 }
 
@@ -695,9 +751,10 @@ hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
     return launch_tile<P>(ortho_tail_tile(rest, cus), part, stream);
 }
 
-// The workspace: X, two transposed copies (one is read while the other is written), A, B and the partial sums.
+// The workspace: X twice (one is read while the other is written), A, B and the partial sums. X has mp rows, zeros behind its m: B X
+// contracts over them.
 struct Layout {
-    int64_t m, n, mp, np, x, t0, t1, a, b, partial, bytes;
+    int64_t m, n, mp, np, x0, x1, a, b, partial, bytes;
     Layout(int64_t batch, int64_t N, int64_t K) : m(std::min(N, K)), n(std::max(N, K)), mp(pad(m)), np(pad(n)) {
         int64_t at = 0;
         auto take = [&](int64_t size) {
@@ -705,9 +762,8 @@ struct Layout {
             at += align256(size);
             return here;
         };
-        x = take(2 * batch * m * np);
-        t0 = take(2 * batch * n * mp);
-        t1 = take(2 * batch * n * mp);
+        x0 = take(2 * batch * mp * np);
+        x1 = take(2 * batch * mp * np);
         a = take(2 * batch * m * mp);
         b = take(2 * batch * m * mp);
         partial = take(8 * batch * kNormParts);
@@ -722,20 +778,20 @@ int64_t fg_ortho_workspace_bytes(int64_t batch, int64_t N, int64_t K) { return L
 hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
     const Layout l(o.batch, o.N, o.K);
     uint8_t* ws = (uint8_t*)o.workspace;
-    uint16_t *x = (uint16_t*)(ws + l.x), *t = (uint16_t*)(ws + l.t0), *t_next = (uint16_t*)(ws + l.t1);
-    uint16_t *a = (uint16_t*)(ws + l.a), *b = (uint16_t*)(ws + l.b);
+    uint16_t *x = (uint16_t*)(ws + l.x0), *next = (uint16_t*)(ws + l.x1), *a = (uint16_t*)(ws + l.a), *b = (uint16_t*)(ws + l.b);
     double* partial = (double*)(ws + l.partial);
     const bool wide = o.N <= o.K;
     const int parts = (int)std::min<int64_t>(kNormParts, (o.N * ((o.K + 3) / 4) + 2 * kNormThreads - 1) / (2 * kNormThreads));
     hipLaunchKernelGGL(fg_ortho_norm_kernel, dim3(parts, (unsigned)o.batch), dim3(kNormThreads), 0, stream, o, partial);
-    hipLaunchKernelGGL(fg_ortho_start_kernel, dim3((unsigned)(((o.N + 63) / 64) * ((o.K + 63) / 64)), (unsigned)o.batch), dim3(256), 0, stream,
-                       o, partial, parts, wide ? x : t, wide ? t : x, wide ? l.np : l.mp, wide ? l.mp : l.np);
+    const dim3 blocks((unsigned)(((o.N + 63) / 64) * ((o.K + 63) / 64)), (unsigned)o.batch);
+    if (wide) hipLaunchKernelGGL(fg_ortho_start_kernel<true>, blocks, dim3(256), 0, stream, o, partial, parts, x, next, l.mp, l.np);
+    else hipLaunchKernelGGL(fg_ortho_start_kernel<false>, blocks, dim3(256), 0, stream, o, partial, parts, x, next, l.mp, l.np);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     for (int s = 0; s < o.steps; s++) {
         OrthoGemm g{};
         g.batch = (int)o.batch;
         g.M = g.N = (int)l.m;
-        g.p = g.q = x; g.ld = l.np; g.p_batch = g.q_batch = l.m * l.np;
+        g.p = g.q = x; g.ld = l.np; g.p_batch = g.q_batch = l.mp * l.np;
         g.out = g.out_t = a; g.ld_out = g.ld_t = l.mp; g.out_batch = g.t_batch = l.m * l.mp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
         if (const hipError_t e = launch_gemm<PRODUCT_A>(g, stream); e != hipSuccess) return e;
@@ -743,10 +799,9 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
         g.out = g.out_t = b;
         g.alpha = o.c / kScaleA; g.beta = o.b; g.diag = o.a * kScaleA;
         if (const hipError_t e = launch_gemm<PRODUCT_B>(g, stream); e != hipSuccess) return e;
-        g.p = b; g.q = t; g.q_batch = l.n * l.mp; g.N = (int)l.n;
+        g.p = b; g.q = x; g.ld_q = l.np; g.q_batch = l.mp * l.np; g.N = (int)l.n;
         if (s + 1 < o.steps) {
-            g.out = x; g.ld_out = l.np; g.out_batch = l.m * l.np;
-            g.out_t = t_next; g.ld_t = l.mp; g.t_batch = l.n * l.mp;
+            g.out = next; g.ld_out = l.np; g.out_batch = l.mp * l.np;
             g.alpha = 1.0f / kScaleA;
             if (const hipError_t e = launch_gemm<PRODUCT_X>(g, stream); e != hipSuccess) return e;
         } else {
@@ -756,7 +811,7 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
             g.alpha = o.scale / (kScaleA * kScaleX);
             if (const hipError_t e = launch_gemm<PRODUCT_LAST>(g, stream); e != hipSuccess) return e;
         }
-        std::swap(t, t_next);
+        std::swap(x, next);
     }
     return hipSuccess;
 }
