@@ -18,28 +18,28 @@ inline int64_t ortho_tiles(int64_t batch, int64_t M, int64_t N, bool symmetric, 
 // part (first loads, last stores) and a time for every step that grows with the CUs that are busy (they share caches
 // and power). Measured and (estimated), five symmetric products and four others:
 //                                    64            128          128 in pairs   256
-//   256 x 256, 16 steps              7.8 (8.7)     13.7 (15)    13.6 (16)      22.5 (27)
-//   1024 x 1024, 64                  15.8 (17)     33.8 (35)    41.2 (39)      68.2 (70)
-//   2048 x 2048, 32                  23.8 (24)     22.0 (24)    25.6 (26)      42.3 (44)
-//   4096 x 4096, 64                  163 (165)     111 (116)    98.1 (108)     82.2 (90)
-//   8 of 2048 x 2048, 32             -             120 (115)    101 (100)      111 (105)
-//   1000 x 2001, 16                  13.6 (13)     16.7 (16)    17.9 (17)      32.8 (29)
-//   1536 x 4096, 24                  41.5 (52)     38.2 (39)    31.4 (29)      39.7 (42)
-//   8 of 1024 x 2048, 16             70.0 (100)    60.2 (60)    46.8 (47)      39.6 (43)
-//   8 of 2048 x 7168, 32             -             705 (650)    606 (535)      434 (433)
+//   256 x 256, 16 steps              7.5 (8.7)     14.4 (13)     13.8 (14)     20.6 (24)
+//   1000 x 2001, 16                  12.2 (12)     14.7 (14)     15 (15)       23.1 (24)
+//   1024 x 1024, 64                  15.3 (17)     33.2 (34)     40.8 (37)     66.2 (65)
+//   2048 x 2048, 32                  23.6 (22)     21.5 (22)     24.9 (24)     40.1 (38)
+//   1536 x 4096, 24                  37.8 (48)     34.2 (35)     27.2 (27)     34.6 (33)
+//   8 of 1024 x 2048, 16             62.4 (88)     52 (51)       39.7 (43)     34.8 (34)
+//   4096 x 4096, 64                  162 (158)     110 (112)     97.4 (104)    78.3 (77)
+//   8 of 2048 x 2048, 112            -             322 (325)     326 (294)     299 (277)
+//   8 of 2048 x 7168, 32             -             690 (598)     550 (507)     390 (378)
 inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_t cus) {
     const double s = (double)steps;
     if (tile == TILE_64) {                       // one workgroup a CU, or two
         if (tiles <= cus) return 6.0 + 0.17 * s;
         const double fill = (double)tiles / (double)(2 * cus);
-        return fill <= 1.0 ? 4.5 + (0.2 + 0.3 * fill) * s : 1.5 + fill * (3.0 + 0.58 * s);
+        return fill <= 1.0 ? 4.5 + (0.2 + 0.3 * fill) * s : 1.5 + fill * (1.5 + 0.58 * s);
     }
     const int64_t slots = tile == TILE_128_PAIRS ? 2 * cus : cus;
     auto round = [&](double fill) {
         switch (tile) {
-            case TILE_128: return 5.5 + (0.39 + 0.16 * fill) * s;
-            case TILE_128_PAIRS: return 6.0 + (fill <= 0.5 ? 0.45 + 0.3 * fill : 0.7 + 0.6 * (fill - 0.5)) * s;
-            default: return 9.5 + 7.0 * fill + (0.85 + 0.55 * fill) * s;
+            case TILE_128: return 3.0 + (0.42 + 0.15 * fill) * s;
+            case TILE_128_PAIRS: return 4.0 + (fill <= 0.5 ? 0.45 + 0.3 * fill : 0.7 + 0.6 * (fill - 0.5)) * s;
+            default: return 6.0 + fill + (0.85 + 0.1 * fill + 0.5 * fill * fill) * s;
         }
     };
     const int64_t whole = tiles / slots, rest = tiles % slots;
@@ -47,7 +47,8 @@ inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_
 }
 
 // The rest of whole rounds of 256 x 256 tiles, in quarters on 128 x 128 tiles, one or two to a CU. Eight symmetric 2048 x 2048
-// (288 tiles), 112 steps: 250 us in two launches and 301 in one; 32 steps: 91 and 111 (101 on 128 x 128 tiles alone).
+// (288 tiles), 112 steps: 267 us in two launches and 299 in one; 32 steps: 103 and 111 (102 on 128 x 128 tiles alone).
+// (The quarters' contraction split in two, with a third launch for the sums: 64 us instead of 72, and 38 instead of 29.)
 inline OrthoTile ortho_tail_tile(int64_t rest, int64_t cus) { return 4 * rest <= cus ? TILE_128 : TILE_128_PAIRS; }
 
 inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus) {

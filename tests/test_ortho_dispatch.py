@@ -10,15 +10,15 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
 
 # batch, M, N, symmetric, steps: measured on tiles of 64, 128, 128 in pairs and 256
-MEASURED = {(1, 256, 256, 1, 16): (7.8, 13.7, 13.6, 22.5), (1, 256, 256, 1, 4): (5.0, 9.7, 9.2, 16.3), (1, 256, 1024, 0, 4): (5.1, 9.0, 8.8, 17.1),
-            (1, 1000, 1000, 1, 32): (10.9, 20.6, 23.4, 40.8), (1, 1000, 2001, 0, 16): (13.6, 16.7, 17.9, 32.8),
-            (1, 512, 512, 1, 8): (6.6, 10.2, 10.5, 19.4), (1, 1024, 1024, 1, 64): (15.8, 33.8, 41.2, 68.2),
-            (1, 1024, 4096, 0, 16): (21.0, 17.4, 18.0, 30.3), (1, 2048, 2048, 1, 32): (23.8, 22.0, 25.6, 42.3),
-            (1, 2048, 2048, 0, 32): (39.4, 25.8, 28.6, 45.5), (1, 1536, 1536, 1, 64): (26.8, 34.8, 42.3, 69.7),
-            (1, 1536, 4096, 0, 24): (41.5, 38.2, 31.4, 39.7), (8, 512, 512, 1, 16): (10.2, 13.8, 13.1, 26.8),
-            (8, 1024, 1024, 1, 32): (35.8, 41.0, 32.3, 44.6), (8, 1024, 2048, 0, 16): (70.0, 60.2, 46.8, 39.6),
-            (1, 4096, 4096, 1, 64): (163, 111, 98.1, 82.2), (1, 4096, 4096, 0, 64): (304, 175, 133, 105.6),
-            (8, 2048, 7168, 0, 32): (None, 705, 606, 434)}
+MEASURED = {(1, 256, 256, 1, 16): (7.5, 14.4, 13.8, 20.6), (1, 256, 256, 1, 4): (5.5, 10.2, 8.6, 15.6),
+            (1, 256, 1024, 0, 4): (4.9, 7.8, 6.6, 11.6), (1, 1000, 1000, 1, 32): (9.8, 22.2, 23.8, 38.6),
+            (1, 1000, 2001, 0, 16): (12.2, 14.7, 15.0, 23.1), (1, 512, 512, 1, 8): (6.4, 10.1, 10.3, 17.2),
+            (1, 1024, 1024, 1, 64): (15.3, 33.2, 40.8, 66.2), (1, 1024, 4096, 0, 16): (19.6, 15.4, 16.4, 24.8),
+            (1, 2048, 2048, 1, 32): (23.6, 21.5, 24.9, 40.1), (1, 2048, 2048, 0, 32): (36.1, 24.1, 26.6, 40.0),
+            (1, 1536, 1536, 1, 64): (26.3, 33.8, 41.6, 67.1), (1, 1536, 4096, 0, 24): (37.8, 34.2, 27.2, 34.6),
+            (8, 512, 512, 1, 16): (10.0, 13.3, 14.1, 24.7), (8, 1024, 1024, 1, 32): (34.4, 39.3, 31.9, 41.7),
+            (8, 1024, 2048, 0, 16): (62.4, 52.0, 39.7, 34.8), (1, 4096, 4096, 1, 64): (162.1, 110.5, 97.4, 78.3),
+            (1, 4096, 4096, 0, 64): (298.9, 166.4, 127.7, 102.7), (8, 2048, 7168, 0, 32): (None, 689.7, 550.1, 390.1)}
 
 
 @pytest.fixture(scope="module")
