@@ -270,7 +270,9 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
 // ------------------------------------------------------------------------------------------------
 // Forward, both tilings and the output: a 512-thread workgroup takes 128 rows x 128 columns and reads x again (from the Infinity
 // Cache where it fits, hence the last rows first), with the statistics of the kernel above. Thread t holds rows 4 (t / 16) + i
-// of the eight columns t % 16: a row's tile is a DPP row, while the columns' maxima and codes go through LDS.
+// of the eight columns t % 16: a row's tile is a DPP row, while the columns' maxima and codes go through LDS. HBM bounds it: 4096
+// x 7168 bf16 22.7 us, x from the cache, 117 MB in all; 4096 x 18432 f32 76.8 us, 453 MB, 5.9 TB/s. The statistics before it: 10.5
+// and 73.9 us (5.6 and 4.1 TB/s).
 // ------------------------------------------------------------------------------------------------
 template <bool LAYER>
 __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {

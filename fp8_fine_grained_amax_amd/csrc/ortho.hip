@@ -376,9 +376,10 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
 // fixed: A0 and B are 6 loads of a wave, A1 2. Past the end every step loads the last block again, into a slot that nobody reads:
 // asking for the end cost 1.5%.
 //
-// Measured: B X of 7168 x 18432, 1.39 ms, 1363 TFLOP/s (torch's fp16 product of these sizes 1.37 ms). The matrix cores are busy
-// 76% of the cycles at about 1.7 GHz, which the chip's power leaves them. Turns of 16 MFMAs (quarters, half the reads a turn)
-// took 10% longer, MFMAs of 32 x 32 5% (fewer cycles, a lower clock).
+// Measured: B X of 7168 x 18432, 1.33 to 1.45 ms by the gradient's values, 1310 to 1426 TFLOP/s (torch's fp16 product of these
+// sizes 1.37 ms). The matrix cores are busy 81% of the cycles at about 1.7 GHz, which the chip's power leaves them; at 8 x 2048 x
+// 7168 66% at 1.8 GHz, 1240 TFLOP/s: there a tile has 32 K steps between its first loads and last stores. Turns of 16 MFMAs
+// (quarters, half the reads a turn) took 10% longer, MFMAs of 32 x 32 5% (fewer cycles, a lower clock).
 // ------------------------------------------------------------------------------------------------
 struct BigTile {
     static constexpr int NTHREADS = 512, BM = 256, BN = 256, MSUB = 8, NSUB = 4, STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
@@ -498,9 +499,10 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
 // ------------------------------------------------------------------------------------------------
 // 64 x 64 workgroup tiles for small matrices: 4 waves, each with a quarter of the contraction (every fourth K step) for the whole
 // tile and stages of its own, so that nothing waits for another wave before the sums are joined, in LDS and in the order of
-// the waves. A CU loads at about 80 to 95 GB/s, and that bounds the K steps: two stages a wave (SLOTS) gain only 5 to 8% over
-// one, which leaves room for a second workgroup on a CU: 256 x 256 x 1024, 10 tiles, 7.8 and 8.3 us; 1000 x 2001 x 1000, 512
-// tiles, 16.0 and 13.6.
+// the waves. A CU loads at about 80 to 95 GB/s, and that bounds the K steps: two stages a wave (SLOTS) gain at most 8% over
+// one, which leaves room for a second workgroup on a CU: two stages and one, 1000 x 1000 x 2001, 136 tiles, 10.2 and 11.0 us;
+// 1000 x 2001 x 1000, 512 tiles, 14.2 and 11.0. The smallest, 256 x 256 x 256, takes 4.9 us, nearly all of it latency: of the launch,
+// the first loads, the join and the stores.
 // ------------------------------------------------------------------------------------------------
 template <int SLOTS_>
 struct SmallTile {
@@ -598,7 +600,7 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 }
 
 // ------------------------------------------------------------------------------------------------
-// The start: |G|, then X.
+// The start: |G|, then X. Both are bound by HBM: 8 x 2048 x 7168 f32 99 us (4.8 TB/s) and 120 (5.9).
 // ------------------------------------------------------------------------------------------------
 // Four neighbouring elements of G from element i on, the first `count` of them; `whole`: all four, aligned to their size.
 __device__ __forceinline__ v4f load_g(const FgOrtho& p, int64_t i, int64_t count, bool whole) {
