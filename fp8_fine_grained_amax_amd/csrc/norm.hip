@@ -57,6 +57,8 @@ __device__ __forceinline__ void store8(void* p, uint32_t i, const float (&f)[8],
     }
 }
 
+typedef float v4f_at4 __attribute__((ext_vector_type(4), aligned(4)));      // the scales' buffer is aligned to its elements only
+
 // Sum over the 16 lanes of a DPP row, in all of them (row_ror 8 and 4, quad_perm [2,3,0,1] and [1,0,3,2]).
 __device__ __forceinline__ float row16_sum(float v) {
 #define FG_STEP(ctrl) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false));
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
         *reinterpret_cast<uint2*>(p.q_cols + (r0 + i) * p.cols + col) = q;
         if (p.y) store8(p.y + (r0 + i) * p.cols, (uint32_t)col, y[i], 1);
     }
-    if (chunk == 0) *reinterpret_cast<float4*>(p.s_cols + g * p.rows + r0) = make_float4(s[0], s[1], s[2], s[3]);
+    if (chunk == 0) *reinterpret_cast<v4f_at4*>(p.s_cols + g * p.rows + r0) = v4f_at4{s[0], s[1], s[2], s[3]};
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         m[e] = 0.0f;

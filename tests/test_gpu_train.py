@@ -73,7 +73,8 @@ def test_norm_shapes(rows, cols, kind):
     check_norm(r, x, gamma, beta if layer else None, layer, 1e-5, False, (rows, cols, kind))
 
 
-@pytest.mark.parametrize("rows,cols", [(128, 128), (256, 640), (384, 1024), (128, 8320), (1280, 256), (128, 18432)])
+@pytest.mark.parametrize("rows,cols", [(128, 128), (256, 640), (384, 1024), (128, 8320), (1280, 256), (128, 18432), (8448, 256),
+                                       (640, 18432)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("pow2", [False, True])
 def test_norm_both_tilings(rows, cols, kind, pow2):
@@ -100,6 +101,33 @@ def test_norm_types(types, beta, kind, tokens):
                                    eps=1e-3, statistics=False)
         assert bare.mean is None and bare.rstd is None and bare.y is None
         assert torch.equal(bare.q_cols, r.q_cols) and torch.equal(bare.s_cols, r.s_cols)
+
+
+def odd(*shape, dtype=torch.float32, fill=float("nan")):
+    """A buffer that begins one element behind an aligned one."""
+    n = 1
+    for d in shape:
+        n *= d
+    return torch.full((n + 1,), fill, dtype=dtype, device=device())[1:].view(*shape)
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_fp32_buffers_aligned_to_their_elements(kind):
+    """Scales, statistics and the weights' gradients need no more than their elements' alignment."""
+    rows, cols, layer = 256, 640, kind == "layer"
+    k = fg.FG_NORM_LAYER if layer else fg.FG_NORM_RMS
+    x, gamma, beta = rows_like(1, rows, cols, torch.bfloat16), 1 + rand(2, cols, std=0.2), rand(3, cols, std=0.1)
+    want = fg.fg_norm_quantize(x, gamma, beta, kind=k, token_tiles=True, with_y=True)
+    out = fg.NormTiles(torch.empty_like(want.q_cols), odd(cols // 128, rows), torch.empty_like(want.q_rows), odd(rows // 128, cols),
+                       torch.empty_like(want.y), odd(rows), odd(rows))
+    got = fg.fg_norm_quantize(x, gamma, beta, kind=k, token_tiles=True, with_y=True, out=out)
+    assert got.s_cols.data_ptr() % 16 == 4
+    for a, b in zip(got, want):
+        assert (a is None and b is None) or torch.equal(a, b)
+    dy = rand(4, rows, cols)
+    grad = fg.fg_norm_bwd(x, want.mean, want.rstd, gamma, dy, kind=k, bias_grad=True)
+    same = fg.fg_norm_bwd(x, got.mean, got.rstd, gamma, dy, kind=k, bias_grad=True, dgamma=odd(cols), dbeta=odd(cols))
+    assert all(torch.equal(a, b) for a, b in zip(same, grad))
 
 
 def test_norm_far_off_centre():
