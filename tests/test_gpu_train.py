@@ -229,6 +229,22 @@ def test_grad_into_its_residual_and_accumulated():
     check_grad(twice, x, mean, rstd, gamma, dy, None, True, "accumulate", before=(3.0, -2.0))
 
 
+@pytest.mark.parametrize("rows,cols", [(70, 384), (40, 5120), (9, 9216), (9, 14336)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_grad_of_either_weight(rows, cols, kind):
+    """dgamma or dbeta alone, and neither: the same numbers as together, whatever way the sums are held and joined."""
+    layer = kind == "layer"
+    x, mean, rstd, gamma, dy = grad_case(rows, cols, layer)
+    args = dict(kind=fg.FG_NORM_LAYER if layer else fg.FG_NORM_RMS)
+    both = fg.fg_norm_bwd(x, mean, rstd, gamma, dy, bias_grad=True, **args)
+    check_grad(both, x, mean, rstd, gamma, dy, None, layer, (rows, cols, kind))
+    for weight, bias in ((True, False), (False, True), (False, False)):
+        r = fg.fg_norm_bwd(x, mean, rstd, gamma, dy, weight_grad=weight, bias_grad=bias, **args)
+        assert torch.equal(r.dx, both.dx) and (r.dgamma is None) != weight and (r.dbeta is None) != bias
+        assert not weight or torch.equal(r.dgamma, both.dgamma)
+        assert not bias or torch.equal(r.dbeta, both.dbeta)
+
+
 def test_grad_of_no_rows():
     e = torch.empty(0, 256, device=device())
     v, nan = torch.empty(0, device=device()), torch.full((256,), float("nan"), device=device())
@@ -334,6 +350,14 @@ def test_update_on_every_tile(batch, n, k, steps):
     for i in {0, batch // 2, batch - 1}:
         ref.check_update(out[i], *ref.orthogonalize(g[i].double(), steps=steps), (n, k, i))
     assert torch.equal(fg.fg_orthogonalize(g, steps=steps), out)
+
+
+@pytest.mark.parametrize("shape", [(96, 200), (3, 200, 64), (1500, 1300)])
+def test_update_in_place(shape):
+    """A bf16 gradient that its own update replaces."""
+    g = torch.stack([gradient(i, *shape[-2:], torch.bfloat16) for i in range(shape[0])]) if len(shape) == 3 else gradient(1, *shape, torch.bfloat16)
+    want = fg.fg_orthogonalize(g)
+    assert fg.fg_orthogonalize(g, out=g) is g and torch.equal(g, want)
 
 
 def test_update_special_matrices():
