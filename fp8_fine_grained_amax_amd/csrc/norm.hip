@@ -69,6 +69,13 @@ __device__ __forceinline__ float row16_sum(float v) {
 #undef FG_STEP
     return v;
 }
+// Sum over a DPP row's lanes l % LANES, in all of them.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    if constexpr (LANES <= 8) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x128, 0xF, 0xF, false));
+    if constexpr (LANES <= 4) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x124, 0xF, 0xF, false));
+    return v;
+}
 __device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
 
 constexpr int kMaxWaves = 16;
@@ -376,16 +383,80 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
 // HBM bounds it: x, dy and the residual's gradient are read once and dx is written (inputs bf16, f32, bf16; dx bf16). Up to
 // 8192 columns the next row is loaded while this one is worked on: 4096 x 7168 58 us, 5.0 TB/s; 16384 x 2048 58 us, 5.7 TB/s
 // (a copy reaches 4.7 to 5.2). With two and three groups a thread the registers do not hold a second row: 4096 x 12288 108 us,
-// 4.7 TB/s, 4096 x 18432 160 us, 4.7 TB/s. 256 x 1024 takes 6.8 us and the sums 2.6: latency of loads, sums and joins.
+// 4.7 TB/s, 4096 x 18432 160 us, 4.7 TB/s. The second launch takes 2.5 to 5 us. Few rows are bound by latency, so they take one
+// launch, in which other workgroups read x and dy once more for the columns' sums.
 // ------------------------------------------------------------------------------------------------
-template <int U, bool LAYER, bool BIAS>
-__global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBwd p, int waves, int64_t rows_each, int64_t partials) {
+// Columns of a workgroup that sums them by itself. 64 and 128: 256 x 1024 f32 5.3 and 6.4 us, 512 x 1024 7.0 and 9.9, 64 x 18432
+// 11.2 and 8.8; 32 the first as 64, the last 12.3.
+constexpr int kSlab = 64;
+// A workgroup's columns of dgamma and dbeta, whole: kSlab / 8 lanes to a row, so 512 / kSlab rows of a wave at a time.
+template <bool LAYER>
+__device__ __forceinline__ void sum_columns(const FgNormBwd& p, int block, float (*sums)[kMaxWaves][kSlab]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = (int)(blockDim.x >> 6);
+    constexpr int LANES = kSlab / 8, ROWS = 64 / LANES;
+    const int64_t col = (int64_t)block * kSlab + 8 * (lane % LANES), step = ROWS * waves;
+    float dg[8] = {}, db[8] = {};
+    constexpr int AT_ONCE = 4;
+    for (int64_t r0 = ROWS * wave + lane / LANES; r0 < p.rows; r0 += AT_ONCE * step) {
+        Raw8 rx[AT_ONCE], rd[AT_ONCE];
+        float rstd[AT_ONCE], mean[AT_ONCE];
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) {
+            const int64_t row = r0 + i * step < p.rows ? r0 + i * step : p.rows - 1;
+            rx[i].load(at_elem(p.x, row * p.ld_x, p.x_bf16), (uint32_t)col, p.x_bf16);
+            rd[i].load(at_elem(p.dy, row * p.ld_dy, p.dy_bf16), (uint32_t)col, p.dy_bf16);
+            rstd[i] = p.rstd[row];
+            mean[i] = LAYER ? p.mean[row] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; i++) {
+            if (r0 + i * step >= p.rows) continue;
+            float x[8], d[8];
+            rx[i].get(x, p.x_bf16);
+            rd[i].get(d, p.dy_bf16);
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                dg[e] += d[e] * ((LAYER ? x[e] - mean[i] : x[e]) * rstd[i]);
+                db[e] += d[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        dg[e] = rows_sum(lanes_sum<LANES>(dg[e]));
+        db[e] = rows_sum(lanes_sum<LANES>(db[e]));
+    }
+    if (lane < LANES) {
+        store8(sums[0][wave], 8 * lane, dg, 0);
+        store8(sums[1][wave], 8 * lane, db, 0);
+    }
+    __syncthreads();
+    const int which = (int)threadIdx.x / kSlab, c = threadIdx.x % kSlab;
+    float* out = which == 0 ? p.dgamma : which == 1 ? p.dbeta : nullptr;
+    if (!out) return;
+    out += (int64_t)block * kSlab + c;
+    float s = p.accumulate ? *out : 0.0f;
+    for (int w = 0; w < waves; w++) s += sums[which][w][c];
+    *out = s;
+}
+
+// SUMS: the rows' workgroups add up the columns, dgamma's and with BIAS dbeta's. Otherwise the first `first` workgroups do that,
+// reading x and dy once more.
+template <int U, bool LAYER, bool SUMS, bool BIAS>
+__global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBwd p, int waves, int64_t rows_each, int64_t partials, int first) {
     constexpr bool AHEAD = U == 1;                  // with more groups the registers do not hold a second row
     __shared__ float part[2][kMaxWaves][2];
-    constexpr bool HELD = U > 2;                    // the columns' sums are held in LDS, dgamma's and then dbeta's
+    if constexpr (!SUMS) {
+        __shared__ float sums[2][kMaxWaves][kSlab];
+        if ((int)blockIdx.x < first) {
+            sum_columns<LAYER>(p, blockIdx.x, sums);
+            return;
+        }
+    }
+    constexpr bool HELD = SUMS && U > 2;            // the columns' sums are held in LDS, dgamma's and then dbeta's
     extern __shared__ __attribute__((aligned(16))) float join[];       // else with more than one group [groups][cols] of dgamma's, then dbeta's
     const Place at(waves, p.cols);
-    const int64_t row0 = (int64_t)blockIdx.x * rows_each;
+    const int64_t row0 = (int64_t)(blockIdx.x - first) * rows_each;
     const int64_t end = row0 + rows_each < p.rows ? row0 + rows_each : p.rows;
     const float inv_n = 1.0f / (float)p.cols;
     // At.past, but asked of all groups after the first: the branches keep the compiler from working on all of them at once, for
@@ -465,7 +536,7 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
                 t1 += t;
                 t2 = __builtin_fmaf(t, h, t2);
             }
-            if (live) {
+            if (SUMS && live) {
                 if constexpr (HELD) {
                     held(join + 8 * (at.t + u * at.span), x);
                     if constexpr (BIAS) held(join + p.cols + 8 * (at.t + u * at.span), d);
@@ -522,7 +593,7 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
             if constexpr (U > 1) __builtin_amdgcn_sched_barrier(0);
         }
     }
-    if (!p.partial) return;
+    if constexpr (!SUMS) return;
     float *out_g = p.partial + (int64_t)blockIdx.x * p.cols, *out_b = p.partial + (partials + (int64_t)blockIdx.x) * p.cols;
     if constexpr (HELD) {
 #pragma unroll
@@ -635,7 +706,18 @@ constexpr int64_t kMaxPartials = 256;
 // and 9.7, 4096 of 7168 24.0 and 22.1.
 constexpr int64_t kFewRows = 256;
 
+// Rows whose backward is one launch, in which workgroups of their own sum the columns, and reads x and dy twice; with more rows the
+// rows' workgroups keep the sums, and a second launch adds them. One and two launches: 64 x 1024 bf16 4.6
+// and 7.5 us, 512 x 1024 5.3 and 8.0, 1024 x 1024 8.0 and 8.8, 2048 x 1024 12.8 and 10.7; f32 256 x 4096 6.6 and 11.0, 512 x 128 5.2
+// and 7.0, 512 x 18432 40.9 and 43.7, 1024 x 128 8.7 and 7.0, 1024 x 4096 16.9 and 16.4.
+constexpr int64_t kFewGradRows = 512;
+
 int bwd_groups(int64_t cols) { return max_waves(groups_of_thread(cols)) / waves_of_row(cols); }
+// Workgroups of the backward's rows, at most.
+int64_t row_blocks(int64_t rows, int64_t cols) {
+    const int64_t groups = bwd_groups(cols);
+    return std::min(kMaxPartials, (rows + groups - 1) / groups);
+}
 
 }  // namespace
 
@@ -666,13 +748,15 @@ hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
 }
 
 int64_t fg_norm_bwd_partials(int64_t rows, int64_t cols) {
-    const int64_t groups = bwd_groups(cols);
-    return std::min(kMaxPartials, (rows + groups - 1) / groups);
+    if (rows <= kFewGradRows) return 0;
+    return row_blocks(rows, cols);
 }
 
 hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream) {
     const int waves = waves_of_row(p.cols), groups = bwd_groups(p.cols);
-    const int64_t most = fg_norm_bwd_partials(p.rows, p.cols);
+    const int64_t most = row_blocks(p.rows, p.cols);
+    const bool weights = p.dgamma || p.dbeta, few = weights && p.rows > 0 && p.rows <= kFewGradRows, sums = weights && !few;
+    const int first = few ? (int)(p.cols / kSlab) : 0;
     int64_t partials = 0;
     if (p.rows > 0) {
         const int64_t each = ((p.rows + most - 1) / most + groups - 1) / groups * groups;
@@ -680,7 +764,7 @@ hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream) {
         const unsigned threads = 64u * waves * groups;
         // the groups' joins, or past 12288 columns the columns' sums
         const bool held = groups_of_thread(p.cols) > 2;
-        const int bytes = (int)p.cols * 4 * (p.dbeta ? 2 : 1) * (held ? 1 : groups > 1 && p.partial ? groups : 0);
+        const int bytes = !sums ? 0 : (int)p.cols * 4 * (p.dbeta ? 2 : 1) * (held ? 1 : groups > 1 ? groups : 0);
         const hipError_t e = by_groups(p.cols, [&](auto u) {
             constexpr int U = decltype(u)::value;
             auto go = [&](auto kern, std::atomic<uint64_t>& limit_set) {
@@ -688,16 +772,20 @@ hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream) {
                     const hipError_t e = fg_set_lds_limit_once((const void*)kern, (int)kFgNormMaxCols * 8, limit_set);
                     if (e != hipSuccess) return e;
                 }
-                hipLaunchKernelGGL(kern, dim3((unsigned)partials), dim3(threads), bytes, stream, p, waves, each, partials);
+                hipLaunchKernelGGL(kern, dim3((unsigned)(first + partials)), dim3(threads), bytes, stream, p, waves, each, partials, first);
                 return hipGetLastError();
             };
-            static std::atomic<uint64_t> limits[4];
-            if (p.dbeta) return p.layer ? go(fg_norm_bwd_kernel<U, true, true>, limits[0]) : go(fg_norm_bwd_kernel<U, false, true>, limits[1]);
-            return p.layer ? go(fg_norm_bwd_kernel<U, true, false>, limits[2]) : go(fg_norm_bwd_kernel<U, false, false>, limits[3]);
+            static std::atomic<uint64_t> limits[6];
+            if (p.layer) {
+                if (!sums) return go(fg_norm_bwd_kernel<U, true, false, false>, limits[0]);
+                return p.dbeta ? go(fg_norm_bwd_kernel<U, true, true, true>, limits[1]) : go(fg_norm_bwd_kernel<U, true, true, false>, limits[2]);
+            }
+            if (!sums) return go(fg_norm_bwd_kernel<U, false, false, false>, limits[3]);
+            return p.dbeta ? go(fg_norm_bwd_kernel<U, false, true, true>, limits[4]) : go(fg_norm_bwd_kernel<U, false, true, false>, limits[5]);
         });
         if (e != hipSuccess) return e;
     }
-    if (!p.dgamma && !p.dbeta) return hipSuccess;
+    if (first > 0 || (!p.dgamma && !p.dbeta)) return hipSuccess;
     hipLaunchKernelGGL(fg_norm_sum_kernel, dim3((unsigned)(p.cols / 64), 2), dim3(kSumWaves * 64), 0, stream, p.partial, partials, p.cols,
                        p.dgamma, p.dbeta, p.accumulate);
     return hipGetLastError();

@@ -108,6 +108,8 @@ fg_status fg_norm_bwd(const void* x, fg_out_dtype x_type, int64_t ld_x, const fl
         return FG_ERR_UNSUPPORTED_SHAPE;
     if (cols == 0 || (rows == 0 && ((!dgamma && !dbeta) || accumulate))) return FG_OK;
     if (rows > 0 && (!x || !rstd || (kind == FG_NORM_LAYER && !mean) || !gamma || !dy || !dx)) return FG_ERR_INVALID_ARG;
+    // x and dy may be read again after dx is written
+    if (rows > 0 && (dx == x || dx == dy)) return FG_ERR_INVALID_ARG;
     // dx as its own addend is read where it is written; with another type or stride it would be overwritten first
     if (dres && dres == dx && (dres_type != dx_type || ld_dres != cols)) return FG_ERR_INVALID_ARG;
     const int64_t need = dgamma || dbeta ? fg_norm_bwd_workspace(rows, cols) : 0;

@@ -38,7 +38,7 @@ struct FgOrtho {
 
 hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream);
 hipError_t fg_launch_norm_bwd(const FgNormBwd& p, hipStream_t stream);
-int64_t fg_norm_bwd_partials(int64_t rows, int64_t cols);      // rows of partial sums: of dgamma's, and as many of dbeta's
+int64_t fg_norm_bwd_partials(int64_t rows, int64_t cols);      // rows of partial sums: of dgamma's, and as many of dbeta's; 0 with few rows
 hipError_t fg_launch_orthogonalize(const FgOrtho& p, hipStream_t stream);
 int64_t fg_ortho_workspace_bytes(int64_t batch, int64_t N, int64_t K);
 

@@ -52,8 +52,8 @@ fg_status fg_norm_quantize(const void* x, fg_out_dtype x_type, int64_t ld_x, int
  *   dx        [rows][cols] of type dx_type, rounded once from fp32.
  *   dgamma, dbeta  f32 [cols] each, or NULL: not computed. accumulate != 0: added to what they hold. The rows are added up
  *             in an order that depends on the sizes only.
- *   workspace fg_norm_bwd_workspace(rows, cols) bytes, 16-byte aligned, read and written only where dgamma or dbeta is
- *             there; may be NULL where neither is.
+ *   workspace fg_norm_bwd_workspace(rows, cols) bytes (0 up to 512 rows), 16-byte aligned, read and written only where
+ *             dgamma or dbeta is there; may be NULL where neither is, and where it has no bytes.
  *   cols % 128 == 0, cols <= 18432, rows <= 2^25. x, gamma, dy, dres, dx 16-byte aligned, row strides multiples of 16 bytes;
  *   the fp32 vectors 4-byte aligned. rows == 0: no-op, but for dgamma and dbeta, which become 0 (or stay, with accumulate).
  *   cols == 0 is a no-op. Outputs and workspace must not overlap the inputs (but dx dres) or each other. */

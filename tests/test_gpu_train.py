@@ -187,7 +187,7 @@ def grad_case(rows, cols, layer, x_type=torch.bfloat16, dy_type=torch.float32):
     return x, mean.float() if layer else None, rstd.float(), gamma, rand(7, rows, cols, std=1e-3).to(dy_type)
 
 
-@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(3000, 128), (2100, 2048)])
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES + [(3000, 128), (2100, 2048), (511, 1024), (512, 2176), (513, 8192), (530, 12288), (520, 16512)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_grad_shapes(rows, cols, kind):
     layer = kind == "layer"
@@ -215,8 +215,8 @@ def test_grad_types(types, kind):
     check_grad(r, x, mean, rstd, gamma, dy, dres, layer, types)
 
 
-def test_grad_into_its_residual_and_accumulated():
-    rows, cols = 300, 1024
+@pytest.mark.parametrize("rows,cols", [(300, 1024), (900, 1024), (40, 14336), (530, 14336)])
+def test_grad_into_its_residual_and_accumulated(rows, cols):
     x, mean, rstd, gamma, dy = grad_case(rows, cols, True)
     for dtype in T.values():
         dres = rand(9, rows, cols, std=2e-3).to(dtype)
@@ -229,7 +229,7 @@ def test_grad_into_its_residual_and_accumulated():
     check_grad(twice, x, mean, rstd, gamma, dy, None, True, "accumulate", before=(3.0, -2.0))
 
 
-@pytest.mark.parametrize("rows,cols", [(70, 384), (40, 5120), (9, 9216), (9, 14336)])
+@pytest.mark.parametrize("rows,cols", [(70, 384), (40, 5120), (9, 9216), (9, 14336), (512, 128), (513, 128), (600, 640), (520, 5120), (515, 9216), (513, 14336)])
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_grad_of_either_weight(rows, cols, kind):
     """dgamma or dbeta alone, and neither: the same numbers as together, whatever way the sums are held and joined."""

@@ -195,7 +195,10 @@ def test_norm_backward_refusals():
     refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, dx=dy[:-1]), "dx")
     refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, accumulate=True), "accumulate")
     refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, bias_grad=True, accumulate=True, dgamma=gamma.clone()), "accumulate")
-    refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, workspace=torch.empty(16, dtype=torch.uint8, device=device())), "invalid")
+    refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, dx=dy), "invalid")
+    refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, dx=x), "invalid")
+    more = grad_case(600, 256, True)
+    refused(lambda: fg.fg_norm_bwd(*more, workspace=torch.empty(16, dtype=torch.uint8, device=device())), "invalid")
     refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, workspace=gamma), "uint8")
     wide = torch.zeros(130, 512, device=device())
     refused(lambda: fg.fg_norm_bwd(x, mean, rstd, gamma, dy, residual_grad=wide[:, :256], dx=wide[:, :256]), "dx")

@@ -53,9 +53,9 @@ def test_norm_rejections(L):
 
 
 def test_norm_backward_rejections(L):
-    need = L.fg_norm_bwd_workspace(4, 256)
+    need = L.fg_norm_bwd_workspace(600, 256)
 
-    def f(x=A, xt=1, ldx=256, mean=A, rstd=A, gamma=A, wt=0, dy=A, dyt=0, lddy=256, dres=None, rt=0, ldr=256, rows=4, cols=256, kind=0,
+    def f(x=A, xt=1, ldx=256, mean=A, rstd=A, gamma=A, wt=0, dy=A, dyt=0, lddy=256, dres=None, rt=0, ldr=256, rows=600, cols=256, kind=0,
           dx=B, dxt=0, dg=B, db=B, acc=0, ws=B, nws=need):
         return L.fg_norm_bwd(x, xt, ldx, mean, rstd, gamma, wt, dy, dyt, lddy, dres, rt, ldr, rows, cols, kind, dx, dxt, dg, db, acc, ws,
                              nws, None)
@@ -64,6 +64,7 @@ def test_norm_backward_rejections(L):
     assert f(acc=2) == INVALID and f(nws=-1) == INVALID and f(dres=A, rt=2) == INVALID and f(dres=A, ldr=255) == INVALID
     assert f(x=None) == INVALID and f(mean=None) == INVALID and f(rstd=None) == INVALID and f(gamma=None) == INVALID
     assert f(dy=None) == INVALID and f(dx=None) == INVALID and f(ws=None) == INVALID and f(nws=need - 1) == INVALID
+    assert f(dx=A, dy=B) == INVALID and f(dx=A, x=B) == INVALID                   # dx in place of x or dy
     assert f(dres=B, rt=1, dxt=0) == INVALID and f(dres=B, ldr=264) == INVALID     # dx as its own addend, laid out otherwise
     assert f(cols=200) == SHAPE and f(cols=18560, ldx=18560, lddy=18560) == SHAPE and f(rows=(1 << 25) + 1) == SHAPE
     assert f(ldx=1 << 41) == SHAPE and f(lddy=1 << 41) == SHAPE and f(dres=A, ldr=1 << 41) == SHAPE
@@ -93,7 +94,7 @@ def test_update_rejections(L):
 def test_workspace_sizes(L):
     w = L.fg_norm_bwd_workspace
     assert w(0, 256) == 0 and w(-1, 256) == 0 and w(4, 200) == 0 and w(4, 18560) == 0 and w(1 << 40, 256) == 0
-    assert 0 < w(1, 128) <= w(4096, 128) and w(1 << 25, 18432) <= 2 * 256 * 18432 * 4
+    assert w(1, 128) == w(512, 18432) == 0 < w(513, 128) <= w(4096, 128) and w(1 << 25, 18432) <= 2 * 256 * 18432 * 4
     o = L.fg_orthogonalize_workspace
     assert o(0, 8, 8) == 0 and o(1, 0, 8) == 0 and o(1, 65537, 8) == 0 and o(1 << 40, 8, 8) == 0 and o(1, -5, 8) == 0
     assert o(1, 100, 200) == o(1, 200, 100) and o(1, 64, 64) < o(2, 64, 64) < o(2, 64, 128)

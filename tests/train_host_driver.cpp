@@ -40,7 +40,7 @@ int main() {
                         EXPECT(need >= 0 && need <= 2 * 256 * 18432 * 4);
                         const int middle = launches;
                         const fg_status b = fg_norm_bwd(a, (fg_out_dtype)type, ld, f, f, a, FG_OUT_F32, a, FG_OUT_BF16, cols, a + 4096, FG_OUT_BF16, ld,
-                                                        rows, cols, FG_NORM_RMS, a, FG_OUT_F32, f, f, 0, a, need, nullptr);
+                                                        rows, cols, FG_NORM_RMS, a + 64, FG_OUT_F32, f, f, 0, a, need, nullptr);
                         EXPECT(launches == middle || b == FG_OK);
                         accepted += s == FG_OK && b == FG_OK;
                     }
