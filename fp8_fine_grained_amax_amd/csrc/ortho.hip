@@ -33,21 +33,23 @@ constexpr int kNormParts = 256;                  // partial sums of a matrix's s
 int64_t pad(int64_t v) { return (v + BK - 1) / BK * BK; }
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// A step's products. A and B are symmetric: out and out_t are the same matrix. The last X leaves as bf16 without padding; the
-// others are fp16 with zeros up to their strides. Each has kernels of its own: a small product's time is mostly that of code
-// that runs once, and a kernel for all of them has twice as much of it.
+// A step's products. A and B are symmetric and write each tile twice. The last X leaves as bf16 without padding; the others are
+// fp16 with zeros up to their strides. Each has kernels of its own: a small product's time is mostly that of code that
+// runs once, and a kernel for all of them has twice as much of it.
 enum Product { PRODUCT_A, PRODUCT_B, PRODUCT_X, PRODUCT_LAST };
 constexpr bool symmetric(Product P) { return P == PRODUCT_A || P == PRODUCT_B; }
 
-// C = alpha P Q^T of every matrix of a batch; in B beta E + diag I beside it, E of the same shape.
+// C = alpha P Q^T of every matrix of a batch; in B, where Q is P, beta P + diag I beside it. A launch begins with the arguments' way
+// from the host's memory: 168 bytes of them instead of 104 cost a small product 0.1 to 0.2 us.
 struct OrthoGemm {
-    const uint16_t *p, *q, *e;                   // fp16 [M][ld], of A and B [N][ld], of X [ld][ld_q], [M][ld_e]
-    uint16_t *out, *out_t;                       // [M][ld_out] and, of A and B the same, [N][ld_t]; X has the first only, the last one either
-    int64_t p_batch, q_batch, e_batch, out_batch, t_batch;
-    int64_t ld, ld_q, ld_e, ld_out, ld_t;
-    int M, N, batch;
+    const uint16_t *p, *q;                       // fp16 [M][ld]; of A and B [N][ld], of X [ld][ld_q]
+    uint16_t* out;                               // [M][ld_out], or turned [N][ld_out]
+    int64_t p_batch, q_batch, out_batch;
+    int ld, ld_q, ld_out, M, N;
     float alpha, beta, diag;
     int first, count;                            // the 256 x 256 tiles to compute, on tiles of 128 in quarters; count 0: everything
+    int turned;                                  // of the last product only
+    int tiles, m_tiles;                          // of a matrix, and rows of them; tiles of 256 with a count
 };
 
 __device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
@@ -77,12 +79,24 @@ __device__ __forceinline__ int xcd_remap(int b, int total) {
     return x * base + (x < extra ? x : extra) + (b >> 3);
 }
 
-// Tile number id of a lower triangle, row by row.
+// Tile number id (below 2^24) of a lower triangle, row by row: the root is off by one at most.
 __device__ __forceinline__ void triangle(int id, int& i, int& j) {
-    i = (int)((__builtin_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
-    while ((i + 1) * (i + 2) / 2 <= id) i++;
-    while (i * (i + 1) / 2 > id) i--;
+    i = (int)((__builtin_amdgcn_sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
+    i -= i * (i + 1) / 2 > id;
+    i += (i + 1) * (i + 2) / 2 <= id;
     j = id - i * (i + 1) / 2;
+}
+// Matrix and tile number id of a batch; of a symmetric product's lower triangle.
+template <Product P>
+__device__ __forceinline__ void plain_tile(const OrthoGemm& p, int id, int64_t& batch, int& ti, int& tj) {
+    const int b = id / p.tiles, local = id - b * p.tiles;
+    batch = b;
+    if constexpr (symmetric(P)) {
+        triangle(local, ti, tj);
+    } else {
+        tj = local / p.m_tiles;
+        ti = local - tj * p.m_tiles;
+    }
 }
 
 // Byte of 16-byte chunk c of a row below 16 in a stage. An operand of 16 rows and 32 of the 64 values has row l % 16 and eight of
@@ -105,17 +119,17 @@ __device__ __forceinline__ uint32_t q_offset(const OrthoGemm& p, int n0, int f, 
         return (uint32_t)r * (uint32_t)(p.ld * 2) + (((lane & 7) ^ swz128(row)) << 4);
     } else {
         constexpr int CH = BN / 8;
-        const int row = f * (64 / CH) + lane / CH, c = 8 * ((lane % CH) ^ (2 * turn_pair<BN>(row))), last = (int)p.ld_q - 8 - n0;
+        const int row = f * (64 / CH) + lane / CH, c = 8 * ((lane % CH) ^ (2 * turn_pair<BN>(row))), last = p.ld_q - 8 - n0;
         return (uint32_t)row * (uint32_t)(p.ld_q * 2) + 2 * (uint32_t)(c < last ? c : last);
     }
 }
 // The tile's part of the second operand, and the bytes from a K step of it to the next.
 template <Product P>
 __device__ __forceinline__ const uint8_t* q_first(const OrthoGemm& p, int64_t batch, int n0) {
-    return (const uint8_t*)(p.q + batch * p.q_batch + (symmetric(P) ? (int64_t)n0 * p.ld : n0));
+    return (const uint8_t*)(symmetric(P) ? p.p + batch * p.p_batch + (int64_t)n0 * p.ld : p.q + batch * p.q_batch + n0);
 }
 template <Product P>
-__device__ __forceinline__ int64_t q_step(const OrthoGemm& p) { return symmetric(P) ? 2 * BK : 2 * BK * p.ld_q; }
+__device__ __forceinline__ int64_t q_step(const OrthoGemm& p) { return symmetric(P) ? 2 * BK : 2 * BK * (int64_t)p.ld_q; }
 
 // Where a lane finds the operand of 16 columns, first / 16 + j of the tile, in a stage, and the operand's eight values of half h.
 template <Product P, int BN>
@@ -135,13 +149,13 @@ __device__ __forceinline__ v8h read_q(const uint8_t* st, int at, int h) {
 // The 256 x 256 tile number id of a batch.
 template <Product P>
 __device__ __forceinline__ void big_tile(const OrthoGemm& p, int id, int64_t& batch, int& ti, int& tj) {
-    const int m_tiles = (p.M + 255) / 256, n_tiles = (p.N + 255) / 256;
-    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles, local = id % per;
-    batch = id / per;
+    const int b = id / p.tiles, local = id - b * p.tiles;
+    batch = b;
     if constexpr (symmetric(P)) {
         triangle(local, ti, tj);
     } else {
         constexpr int GM = 8;                            // rows of tiles that an XCD's run goes down together
+        const int m_tiles = p.m_tiles, n_tiles = (p.N + 255) / 256;
         const int group = local / (GM * n_tiles), first = group * GM, rows = min(m_tiles - first, GM), within = local - group * GM * n_tiles;
         ti = first + within % rows;
         tj = within / rows;
@@ -156,21 +170,21 @@ __device__ __forceinline__ void wait_loads() {
 template <class T>
 __device__ __forceinline__ uint32_t half_bits(float v) { return (uint32_t)__builtin_bit_cast(unsigned short, (T)v); }
 
-// E's elements of a wave's 16 x 16 tiles, four to a lane, loaded together (in bounds). (wr, wc): the wave's first row and column
+// P's elements at the places of a wave's 16 x 16 tiles of B, four to a lane, loaded together (in bounds). (wr, wc): the wave's first row and column
 // in the workgroup's tile.
 template <Product P, int MSUB, int NSUB>
 __device__ __forceinline__ void load_e(const OrthoGemm& p, uint2 (&w)[MSUB][NSUB], int64_t batch, int m0, int n0, int wr, int wc) {
     if constexpr (P != PRODUCT_B) return;
     const int lane = threadIdx.x & 63;
-    const uint16_t* e = p.e + batch * p.e_batch + (int64_t)m0 * p.ld_e;
+    const uint16_t* e = p.p + batch * p.p_batch + (int64_t)m0 * p.ld;
 #pragma unroll
     for (int i = 0; i < MSUB; i++) {
         const int r = wr + 16 * i + (lane & 15);
-        const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld_e;
+        const uint32_t row = (uint32_t)(m0 + r < p.M ? r : p.M - 1 - m0) * (uint32_t)p.ld;
 #pragma unroll
         for (int j = 0; j < NSUB; j++) {
             const int n = n0 + wc + 16 * j + 4 * (lane >> 4);
-            w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld_e ? n : 0)));
+            w[i][j] = *reinterpret_cast<const uint2*>(e + (row + (uint32_t)(n < p.ld ? n : 0)));
         }
     }
 }
@@ -210,8 +224,8 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
     }
     __syncthreads();
     // 8 values to a lane; `width`: columns that are there. Without padding rows may begin anywhere.
-    auto store = [&](uint16_t* row, int64_t ld, int c, int width, uint4 v) {
-        if (LAST && ((ld & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
+    auto store = [&](uint16_t* row, int c, int width, uint4 v) {
+        if (LAST && ((p.ld_out & 7) || ((uintptr_t)row & 15) || c + 8 > width)) {
             const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 8; k++)
@@ -220,21 +234,21 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
             *reinterpret_cast<uint4*>(row + c) = v;
         }
     };
-    if (P != PRODUCT_LAST || p.out) {
+    if (P != PRODUCT_LAST || !p.turned) {
         constexpr int CH = BN / 8;
         uint16_t* out = p.out + batch * p.out_batch;
-        const int width = LAST ? p.N : (int)p.ld_out;
+        const int width = LAST ? p.N : p.ld_out;
 #pragma unroll 4
         for (int it = 0; it < BM * CH / THREADS; it++) {
             const int f = it * THREADS + tid, r = f / CH, c = f % CH;
             if (m0 + r < p.M)
-                store(out + (int64_t)(m0 + r) * p.ld_out, p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & MIX)) << 4)));
+                store(out + (int64_t)(m0 + r) * p.ld_out, n0 + 8 * c, width, *reinterpret_cast<const uint4*>(smem + r * (2 * BN) + ((c ^ (r & MIX)) << 4)));
         }
     }
-    if (P != PRODUCT_X && p.out_t && !diagonal) {
+    if (LAST ? p.turned : symmetric(P) && !diagonal) {
         constexpr int CH = BM / 8;
-        uint16_t* out = p.out_t + batch * p.t_batch;
-        const int width = LAST ? p.M : (int)p.ld_t;
+        uint16_t* out = p.out + batch * p.out_batch;
+        const int width = LAST ? p.M : p.ld_out;
 #pragma unroll 4
         for (int it = 0; it < BN * CH / THREADS; it++) {
             const int f = it * THREADS + tid, c0 = f / (16 * CH) * 16, r = 8 * (f / 16 % CH), col = c0 + 4 * (lrow & 3);     // column c0 + lrow, rows r .. r + 7
@@ -245,7 +259,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
                 part[h] = tr_read(smem + row * (2 * BN) + (((col >> 3) ^ (row & MIX)) << 4) + ((col >> 2) & 1) * 8);
             }
             const int n = n0 + c0 + lrow;
-            if (n < p.N) store(out + (int64_t)n * p.ld_t, p.ld_t, m0 + r, width, make_uint4(part[0].x, part[0].y, part[1].x, part[1].y));
+            if (n < p.N) store(out + (int64_t)n * p.ld_out, m0 + r, width, make_uint4(part[0].x, part[0].y, part[1].x, part[1].y));
         }
     }
 }
@@ -263,23 +277,18 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int m_tiles = (p.M + C::BM - 1) / C::BM, n_tiles = (p.N + C::BN - 1) / C::BN;
-    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
     int ti, tj;
     int64_t batch;
     if (p.count) {                                       // quarters of 256 x 256 tiles
-        const int id = xcd_remap((int)blockIdx.x, 4 * p.count);
+        const int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
         big_tile<P>(p, p.first + (id >> 2), batch, ti, tj);
         ti = 2 * ti + (id >> 1 & 1);
         tj = 2 * tj + (id & 1);
-        if (ti >= m_tiles || tj >= n_tiles || (symmetric(P) && tj > ti)) return;
+        if (ti * C::BM >= p.M || tj * C::BN >= p.N || (symmetric(P) && tj > ti)) return;
     } else {
-        const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
-        batch = id / per;
-        if constexpr (symmetric(P)) triangle(local, ti, tj);
-        else ti = local % m_tiles, tj = local / m_tiles;
+        plain_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
     }
-    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
+    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = p.ld / BK;
     const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
 
     uint32_t a_off[4], b_off[4];
@@ -394,7 +403,7 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     int64_t batch;
     int ti, tj;
     big_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
-    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = (int)(p.ld / BK);
+    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = p.ld / BK;
     const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
 
     // Loads: an instruction fills 8 rows of 128 bytes. A0 is rows [0, 64) and [128, 192) of the tile; a wave loads 16 rows of
@@ -515,14 +524,10 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
     using C = SmallTile<SLOTS>;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int m_tiles = (p.M + C::SIDE - 1) / C::SIDE, n_tiles = (p.N + C::SIDE - 1) / C::SIDE;
-    const int per = symmetric(P) ? m_tiles * (m_tiles + 1) / 2 : m_tiles * n_tiles;
-    const int id = xcd_remap((int)blockIdx.x, per * p.batch), local = id % per;
-    const int64_t batch = id / per;
+    int64_t batch;
     int ti, tj;
-    if constexpr (symmetric(P)) triangle(local, ti, tj);
-    else ti = local % m_tiles, tj = local / m_tiles;
-    const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = (int)(p.ld / BK);
+    plain_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
+    const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = p.ld / BK;
     const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
     uint8_t* ring = smem + wave * (SLOTS * C::STAGE);
 
@@ -724,33 +729,36 @@ hipError_t launch(Kernel kern, int64_t tiles, int lds, std::atomic<uint64_t>& li
 }
 
 template <Product P>
-hipError_t launch_tile(OrthoTile tile, const OrthoGemm& p, hipStream_t stream) {
+hipError_t launch_tile(OrthoTile tile, const OrthoGemm& all, int64_t batch, hipStream_t stream) {
     static std::atomic<uint64_t> limits[5];
-    auto tiles = [&](int side) { return ortho_tiles(p.batch, p.M, p.N, symmetric(P), side); };
-    const int64_t quarters = p.count ? 4 * (int64_t)p.count : tiles(128);
+    const int side = tile == TILE_64 ? 64 : tile == TILE_256 || all.count ? 256 : 128;
+    OrthoGemm p = all;
+    p.tiles = (int)ortho_tiles(1, p.M, p.N, symmetric(P), side);
+    p.m_tiles = (p.M + side - 1) / side;
+    const int64_t tiles = p.tiles * batch, mid = p.count ? 4 * (int64_t)p.count : tiles;
     switch (tile) {
         case TILE_64:
-            if (tiles(64) <= fg_device_cus())
-                return launch<SmallTile<2>>(fg_ortho_small_kernel<P, 2>, tiles(64), SmallTile<2>::LDS, limits[0], p, stream);
-            return launch<SmallTile<1>>(fg_ortho_small_kernel<P, 1>, tiles(64), SmallTile<1>::LDS, limits[1], p, stream);
-        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<P, 4>, quarters, 4 * MidTile::STAGE, limits[2], p, stream);
-        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<P, 2>, quarters, 2 * MidTile::STAGE, limits[3], p, stream);
-        default: return launch<BigTile>(fg_ortho_big_kernel<P>, p.count ? p.count : tiles(256), BigTile::LDS, limits[4], p, stream);
+            if (tiles <= fg_device_cus())
+                return launch<SmallTile<2>>(fg_ortho_small_kernel<P, 2>, tiles, SmallTile<2>::LDS, limits[0], p, stream);
+            return launch<SmallTile<1>>(fg_ortho_small_kernel<P, 1>, tiles, SmallTile<1>::LDS, limits[1], p, stream);
+        case TILE_128: return launch<MidTile>(fg_ortho_mid_kernel<P, 4>, mid, 4 * MidTile::STAGE, limits[2], p, stream);
+        case TILE_128_PAIRS: return launch<MidTile>(fg_ortho_mid_kernel<P, 2>, mid, 2 * MidTile::STAGE, limits[3], p, stream);
+        default: return launch<BigTile>(fg_ortho_big_kernel<P>, p.count ? p.count : tiles, BigTile::LDS, limits[4], p, stream);
     }
 }
 
 template <Product P>
-hipError_t launch_gemm(const OrthoGemm& p, hipStream_t stream) {
+hipError_t launch_gemm(const OrthoGemm& p, int64_t batch, hipStream_t stream) {
     const int64_t cus = fg_device_cus();
-    const OrthoTile tile = ortho_tile(p.batch, p.M, p.N, symmetric(P), p.ld / BK, cus);
-    if (tile != TILE_256_TAIL) return launch_tile<P>(tile, p, stream);
-    const int64_t all = ortho_tiles(p.batch, p.M, p.N, symmetric(P), 256), rest = all % cus;
+    const OrthoTile tile = ortho_tile(batch, p.M, p.N, symmetric(P), p.ld / BK, cus);
+    if (tile != TILE_256_TAIL) return launch_tile<P>(tile, p, batch, stream);
+    const int64_t all = ortho_tiles(batch, p.M, p.N, symmetric(P), 256), rest = all % cus;
     OrthoGemm part = p;
     part.count = (int)(all - rest);
-    if (const hipError_t e = launch_tile<P>(TILE_256, part, stream); e != hipSuccess) return e;
+    if (const hipError_t e = launch_tile<P>(TILE_256, part, batch, stream); e != hipSuccess) return e;
     part.first = part.count;
     part.count = (int)rest;
-    return launch_tile<P>(ortho_tail_tile(rest, cus), part, stream);
+    return launch_tile<P>(ortho_tail_tile(rest, cus), part, batch, stream);
 }
 
 // The workspace: X twice (one is read while the other is written), A, B and the partial sums. X has mp rows, zeros behind its m: B X
@@ -791,27 +799,25 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     for (int s = 0; s < o.steps; s++) {
         OrthoGemm g{};
-        g.batch = (int)o.batch;
         g.M = g.N = (int)l.m;
-        g.p = g.q = x; g.ld = l.np; g.p_batch = g.q_batch = l.mp * l.np;
-        g.out = g.out_t = a; g.ld_out = g.ld_t = l.mp; g.out_batch = g.t_batch = l.m * l.mp;
+        g.p = x; g.ld = (int)l.np; g.p_batch = l.mp * l.np;
+        g.out = a; g.ld_out = (int)l.mp; g.out_batch = l.m * l.mp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
-        if (const hipError_t e = launch_gemm<PRODUCT_A>(g, stream); e != hipSuccess) return e;
-        g.p = g.q = g.e = a; g.ld = g.ld_e = l.mp; g.p_batch = g.q_batch = g.e_batch = l.m * l.mp;
-        g.out = g.out_t = b;
+        if (const hipError_t e = launch_gemm<PRODUCT_A>(g, o.batch, stream); e != hipSuccess) return e;
+        g.p = a; g.ld = (int)l.mp; g.p_batch = l.m * l.mp;
+        g.out = b;
         g.alpha = o.c / kScaleA; g.beta = o.b; g.diag = o.a * kScaleA;
-        if (const hipError_t e = launch_gemm<PRODUCT_B>(g, stream); e != hipSuccess) return e;
-        g.p = b; g.q = x; g.ld_q = l.np; g.q_batch = l.mp * l.np; g.N = (int)l.n;
+        if (const hipError_t e = launch_gemm<PRODUCT_B>(g, o.batch, stream); e != hipSuccess) return e;
+        g.p = b; g.q = x; g.ld_q = (int)l.np; g.q_batch = l.mp * l.np; g.N = (int)l.n;
         if (s + 1 < o.steps) {
-            g.out = next; g.ld_out = l.np; g.out_batch = l.mp * l.np;
+            g.out = next; g.ld_out = (int)l.np; g.out_batch = l.mp * l.np;
             g.alpha = 1.0f / kScaleA;
-            if (const hipError_t e = launch_gemm<PRODUCT_X>(g, stream); e != hipSuccess) return e;
+            if (const hipError_t e = launch_gemm<PRODUCT_X>(g, o.batch, stream); e != hipSuccess) return e;
         } else {
-            g.out = wide ? o.out : nullptr;
-            g.out_t = wide ? nullptr : o.out;
-            g.ld_out = g.ld_t = o.K; g.out_batch = g.t_batch = o.N * o.K;
+            g.out = o.out; g.ld_out = (int)o.K; g.out_batch = o.N * o.K;
+            g.turned = !wide;
             g.alpha = o.scale / (kScaleA * kScaleX);
-            if (const hipError_t e = launch_gemm<PRODUCT_LAST>(g, stream); e != hipSuccess) return e;
+            if (const hipError_t e = launch_gemm<PRODUCT_LAST>(g, o.batch, stream); e != hipSuccess) return e;
         }
         std::swap(x, next);
     }
