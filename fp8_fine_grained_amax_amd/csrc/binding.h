@@ -4,7 +4,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -113,8 +113,9 @@ int flag(PyObject* o) {
 }
 fg_scale_mode mode(PyObject* pow2) { return flag(pow2) ? FG_SCALE_POW2 : FG_SCALE_FP32; }
 
+// Past torch's dispatcher, which took 0.2 of 0.65 us a tensor.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device d) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(d));
+    return at::Tensor(at::detail::empty_cuda(shape, type, d, std::nullopt));
 }
 // The caller's output buffer, or a new one.
 at::Tensor output(PyObject* o, const char* what, at::ScalarType type, at::IntArrayRef shape, c10::Device d) {

@@ -2,7 +2,7 @@
 // the other entry points (checks of the tensors, allocation of what the caller does not pass, torch's current stream
 // of the tensors' own device) in compiled code, because at a few tokens the interpreter takes longer over it than the
 // kernels take: a call with its outputs cost 10 us (the Linear, one output) to 27 us (the activation's backward, seven)
-// in Python, against 4 to 11 us of kernels; here 5 and 16.
+// in Python, against 4 to 11 us of kernels; here 5 and 13.
 #include "binding.h"
 #include "fp8fg_ffn.h"
 
