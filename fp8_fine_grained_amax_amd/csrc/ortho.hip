@@ -519,16 +519,20 @@ struct SmallTile {
     static constexpr int LDS = SLOTS == 2 ? WAVES * 2 * STAGE : WAVES * STAGE + 8192;
 };
 
-template <Product P, int SLOTS>
-__global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGemm p) {
+// SPLIT: the contraction's part number id / (tiles of all matrices) of `split`; its sums go to `parts`.
+template <Product P, int SLOTS, bool SPLIT>
+__device__ __forceinline__ void small_tile(const OrthoGemm& p, v4f* parts, int split) {
     using C = SmallTile<SLOTS>;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t batch;
     int ti, tj;
-    plain_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
-    const int m0 = ti * C::SIDE, n0 = tj * C::SIDE, nkb = p.ld / BK;
-    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
+    const int id = xcd_remap((int)blockIdx.x, (int)gridDim.x), all = SPLIT ? (int)gridDim.x / split : 0, part = SPLIT ? id / all : 0;
+    plain_tile<P>(p, SPLIT ? id - part * all : id, batch, ti, tj);
+    const int steps = p.ld / BK, k0 = SPLIT ? part * steps / split : 0, nkb = SPLIT ? (part + 1) * steps / split - k0 : steps;
+    const int m0 = ti * C::SIDE, n0 = tj * C::SIDE;
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld) + k0 * 128;
+    const uint8_t* qp = q_first<P>(p, batch, n0) + k0 * q_step<P>(p);
     uint8_t* ring = smem + wave * (SLOTS * C::STAGE);
 
     uint32_t a_off[8], b_off[8];
@@ -601,7 +605,53 @@ __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGem
 #pragma unroll
         for (int w = 1; w < C::WAVES; w++) sum[0][j] += red[((w * C::SUB + wave) * C::SUB + j) * 64 + lane];
     }
-    finish<P, C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, symmetric(P) && ti == tj);
+    if constexpr (SPLIT) {                               // rows of 64, a wave's 16
+        v4f* to = parts + (int64_t)id * (C::SIDE * C::SIDE / 4) + (16 * wave + lrow) * (C::SIDE / 4) + g16;
+#pragma unroll
+        for (int j = 0; j < C::SUB; j++) to[4 * j] = sum[0][j];
+    } else {
+        finish<P, C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, symmetric(P) && ti == tj);
+    }
+}
+template <Product P, int SLOTS>
+__global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGemm p) { small_tile<P, SLOTS, false>(p, nullptr, 1); }
+
+// A of few rows and a long contraction: 64 x 64 tiles that several workgroups share, as many as there are CUs. 64 x 16384, one tile
+// and 256 K steps: 5.8 us and 3.4 for the sum of 32 parts; with one workgroup 34 us.
+__global__ __launch_bounds__(256, 1) void fg_ortho_split_kernel(OrthoGemm p, v4f* parts, int split) {
+    small_tile<PRODUCT_A, 2, true>(p, parts, split);
+}
+// The sum of the parts, in their order, and its end: 16 rows of a tile a workgroup, four columns a thread.
+__global__ __launch_bounds__(256) void fg_ortho_join_kernel(OrthoGemm p, const v4f* __restrict__ parts, int split) {
+    __shared__ __attribute__((aligned(16))) uint16_t turned[64][20];     // [column][row]
+    const int tid = threadIdx.x, all = (int)gridDim.x >> 2, strip = blockIdx.x & 3, r = tid >> 4, c = 4 * (tid & 15);
+    int64_t batch;
+    int ti, tj;
+    plain_tile<PRODUCT_A>(p, blockIdx.x >> 2, batch, ti, tj);
+    const v4f* from = parts + (int64_t)(blockIdx.x >> 2) * 1024 + strip * 256 + tid;
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    int part = 0;
+    for (; part + 8 <= split; part += 8) {
+        v4f v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = from[(int64_t)(part + i) * all * 1024];
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += v[i];
+    }
+    for (; part < split; part++) sum += from[(int64_t)part * all * 1024];
+    const int m = ti * 64 + strip * 16 + r, n = tj * 64 + c;
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) h[k] = m < p.M && n + k < p.N ? half_bits<_Float16>(p.alpha * sum[k]) : 0;
+    uint16_t* out = p.out + batch * p.out_batch;
+    if (m < p.M) *reinterpret_cast<uint2*>(out + (int64_t)m * p.ld_out + n) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    if (ti == tj) return;
+#pragma unroll
+    for (int k = 0; k < 4; k++) turned[c + k][r] = (uint16_t)h[k];
+    __syncthreads();
+    const int col = tid >> 2, r4 = 4 * (tid & 3);
+    if (tj * 64 + col < p.N)
+        *reinterpret_cast<uint2*>(out + (int64_t)(tj * 64 + col) * p.ld_out + ti * 64 + strip * 16 + r4) = *reinterpret_cast<const uint2*>(&turned[col][r4]);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -747,9 +797,23 @@ hipError_t launch_tile(OrthoTile tile, const OrthoGemm& all, int64_t batch, hipS
     }
 }
 
+// parts: what the product does not use otherwise of the workspace, parts_bytes of it.
 template <Product P>
-hipError_t launch_gemm(const OrthoGemm& p, int64_t batch, hipStream_t stream) {
+hipError_t launch_gemm(const OrthoGemm& p, int64_t batch, hipStream_t stream, void* parts = nullptr, int64_t parts_bytes = 0) {
     const int64_t cus = fg_device_cus();
+    if constexpr (P == PRODUCT_A) {
+        const int64_t tiles = ortho_tiles(batch, p.M, p.N, true, 64);
+        const int64_t split = ortho_split(tiles, p.ld / BK, parts_bytes / (tiles * 64 * 64 * 4), cus);
+        if (split > 1) {
+            OrthoGemm g = p;
+            g.tiles = (int)(tiles / batch);
+            static std::atomic<uint64_t> limit;
+            if (const hipError_t e = fg_set_lds_limit_once((const void*)fg_ortho_split_kernel, SmallTile<2>::LDS, limit); e != hipSuccess) return e;
+            hipLaunchKernelGGL(fg_ortho_split_kernel, dim3((unsigned)(tiles * split)), dim3(256), SmallTile<2>::LDS, stream, g, (v4f*)parts, (int)split);
+            hipLaunchKernelGGL(fg_ortho_join_kernel, dim3((unsigned)(4 * tiles)), dim3(256), 0, stream, g, (const v4f*)parts, (int)split);
+            return hipGetLastError();
+        }
+    }
     const OrthoTile tile = ortho_tile(batch, p.M, p.N, symmetric(P), p.ld / BK, cus);
     if (tile != TILE_256_TAIL) return launch_tile<P>(tile, p, batch, stream);
     const int64_t all = ortho_tiles(batch, p.M, p.N, symmetric(P), 256), rest = all % cus;
@@ -797,13 +861,15 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
     if (wide) hipLaunchKernelGGL(fg_ortho_start_kernel<true>, blocks, dim3(256), 0, stream, o, partial, parts, x, next, l.mp, l.np);
     else hipLaunchKernelGGL(fg_ortho_start_kernel<false>, blocks, dim3(256), 0, stream, o, partial, parts, x, next, l.mp, l.np);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    // A's parts may lie where the next X will, as far as its first rows of zeros.
+    const int64_t room = 2 * (l.m == l.mp ? o.batch : 1) * l.m * l.np;
     for (int s = 0; s < o.steps; s++) {
         OrthoGemm g{};
         g.M = g.N = (int)l.m;
         g.p = x; g.ld = (int)l.np; g.p_batch = l.mp * l.np;
         g.out = a; g.ld_out = (int)l.mp; g.out_batch = l.m * l.mp;
         g.alpha = kScaleA / (kScaleX * kScaleX);
-        if (const hipError_t e = launch_gemm<PRODUCT_A>(g, o.batch, stream); e != hipSuccess) return e;
+        if (const hipError_t e = launch_gemm<PRODUCT_A>(g, o.batch, stream, next, room); e != hipSuccess) return e;
         g.p = a; g.ld = (int)l.mp; g.p_batch = l.m * l.mp;
         g.out = b;
         g.alpha = o.c / kScaleA; g.beta = o.b; g.diag = o.a * kScaleA;

@@ -51,6 +51,18 @@ inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_
 // (The quarters' contraction split in two, with a third launch for the sums: 64 us instead of 72, and 38 instead of 29.)
 inline OrthoTile ortho_tail_tile(int64_t rest, int64_t cus) { return 4 * rest <= cus ? TILE_128 : TILE_128_PAIRS; }
 
+// Workgroups that share the contraction of each of a symmetric product's 64 x 64 tiles where there are few tiles, with a second launch
+// that adds their sums; 1: none. `room`: parts of all tiles that the workspace has. The second launch costs about 4.5 us, as much
+// as 26 K steps. A whole update by m x n, with one workgroup a tile and with several: 64 x 2048 (32 steps, 4 parts) 87 and 91 us,
+// 256 x 2048 (4) 105 and 104, 64 x 4096 (8) 106 and 90, 64 x 16384 (32) 221 and 95, 512 x 4096 (7) 152 and 141, two of 496 x 3973
+// (3) 174 and 169, 640 x 10240 (4) 292 and 199, 856 x 11323 (2) 382 and 318.
+inline int64_t ortho_split(int64_t tiles, int64_t steps, int64_t room, int64_t cus) {
+    int64_t split = cus / tiles;
+    if (split > steps / 8) split = steps / 8;
+    if (split > room) split = room;
+    return split > 1 && steps - steps / split >= 40 ? split : 1;
+}
+
 inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus) {
     const OrthoTile shapes[] = {TILE_64, TILE_128, TILE_128_PAIRS, TILE_256};
     const int sides[] = {64, 128, 128, 256};

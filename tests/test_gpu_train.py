@@ -360,6 +360,20 @@ def test_update_in_place(shape):
     assert fg.fg_orthogonalize(g, out=g) is g and torch.equal(g, want)
 
 
+@pytest.mark.parametrize("batch,n,k", [(1, 64, 8192), (2, 76, 16200), (3, 5000, 130), (1, 33, 3003), (4, 60, 4200), (1, 309, 4853), (1, 700, 8192),
+                                       (2, 3973, 496), (1, 856, 11323)])
+def test_update_of_few_rows(batch, n, k):
+    """Long contractions that several workgroups share, as far as the workspace has room for their sums."""
+    g = torch.stack([gradient(i, n, k) for i in range(batch)])
+    out = fg.fg_orthogonalize(g, out=torch.full((batch, n, k), float("nan"), dtype=torch.bfloat16, device=device()),
+                              workspace=dirty_workspace(batch, n, k))
+    for i in range(batch):
+        ref.check_update(out[i], *ref.orthogonalize(g[i].double()), (n, k, i))
+    for _ in range(3):
+        assert torch.equal(fg.fg_orthogonalize(g), out)
+    assert torch.equal(fg.fg_orthogonalize(g.flip(0)).flip(0), out)
+
+
 def test_update_special_matrices():
     """Zeros give zeros, whatever stands beside; a NaN or an infinity stays in its own matrix; scales far from one do not matter."""
     g = torch.stack([gradient(i, 100, 150) for i in range(5)])

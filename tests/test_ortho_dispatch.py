@@ -52,9 +52,16 @@ def test_rest_of_a_round(ask):
     assert (tail, even, few) == (4, 3, 3)
 
 
+def test_split_contractions(ask):
+    # tiles and steps: (1, 256), (3, 64), (10, 32), (36, 64), (55, 160), (105, 177), (136, 256)
+    problems = [(1, 64, 64, 1, 256), (1, 128, 128, 1, 64), (1, 256, 256, 1, 32), (1, 512, 512, 1, 64), (1, 640, 640, 1, 160), (1, 856, 856, 1, 177),
+                (1, 1024, 1024, 1, 256)]
+    assert [int(us[4]) for _, us in ask(problems)] == [32, 8, 1, 7, 4, 2, 1]
+
+
 def test_every_size_has_a_choice(ask):
     sides = (1, 2, 63, 64, 65, 129, 500, 1000, 3000, 8191, 20000, 65536)
     problems = [(b, m, n, int(m == n), (n + 63) // 64) for b in (1, 7, 300, 65535) for m in sides for n in sides
                 if m <= n and b * ((m + 63) // 64) * ((n + 63) // 64) < 1 << 24]
     for problem, (choice, us) in zip(problems, ask(problems)):
-        assert 0 <= choice <= 4 and all(u > 0 for u in us), problem
+        assert 0 <= choice <= 4 and all(u > 0 for u in us) and us[4] <= 256, problem
