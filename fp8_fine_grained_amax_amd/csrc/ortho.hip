@@ -271,15 +271,22 @@ struct MidTile {
     static constexpr int NTHREADS = 256, BM = 128, BN = 128, SUB = 4, STAGE = (BM + BN) * 128, LOADS = 8;
 };
 
-template <Product P, int STAGES>
-__global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_kernel(OrthoGemm p) {
+// SPLIT: as small_tile's.
+template <Product P, int STAGES, bool SPLIT>
+__device__ __forceinline__ void mid_tile(const OrthoGemm& p, v4f* parts, int split) {
     using C = MidTile;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    int ti, tj;
+    int ti, tj, steps = p.ld / BK, part_id = 0, k0 = 0, nkb = steps;
     int64_t batch;
-    if (p.count) {                                       // quarters of 256 x 256 tiles
+    if constexpr (SPLIT) {
+        part_id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+        const int all = (int)gridDim.x / split, part = part_id / all;
+        plain_tile<P>(p, part_id - part * all, batch, ti, tj);
+        k0 = part * steps / split;
+        nkb = (part + 1) * steps / split - k0;
+    } else if (p.count) {                                       // quarters of 256 x 256 tiles
         const int id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
         big_tile<P>(p, p.first + (id >> 2), batch, ti, tj);
         ti = 2 * ti + (id >> 1 & 1);
@@ -288,8 +295,9 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     } else {
         plain_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
     }
-    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = p.ld / BK;
-    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
+    const int m0 = ti * C::BM, n0 = tj * C::BN;
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld) + k0 * 128;
+    const uint8_t* qp = q_first<P>(p, batch, n0) + k0 * q_step<P>(p);
 
     uint32_t a_off[4], b_off[4];
 #pragma unroll
@@ -331,7 +339,7 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
         for (int j = 0; j < C::SUB; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
     uint2 e[C::SUB][C::SUB];
-    load_e<P>(p, e, batch, m0, n0, wm * 64, wn * 64);
+    if constexpr (!SPLIT) load_e<P>(p, e, batch, m0, n0, wm * 64, wn * 64);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < STAGES; s++) issue(s, s);
@@ -368,10 +376,17 @@ __global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_ke
     }
     if (kb < nkb) step(kb, std::integral_constant<int, 0>{});
     __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();                                    // the stages are free
-
-    finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 64, wn * 64, symmetric(P) && ti == tj);
+    if constexpr (SPLIT) {                              // a wave's 64 x 64
+        v4f* to = parts + ((int64_t)part_id * 4 + wave) * 1024 + lane;
+#pragma unroll
+        for (int t = 0; t < C::SUB * C::SUB; t++) to[t * 64] = acc[t / C::SUB][t % C::SUB];
+    } else {
+        __syncthreads();                                // the stages are free
+        finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 64, wn * 64, symmetric(P) && ti == tj);
+    }
 }
+template <Product P, int STAGES>
+__global__ __launch_bounds__(MidTile::NTHREADS, 4 / STAGES) void fg_ortho_mid_kernel(OrthoGemm p) { mid_tile<P, STAGES, false>(p, nullptr, 1); }
 
 // ------------------------------------------------------------------------------------------------
 // 256 x 256 x 64 workgroup tiles: 8 waves (2 x 4) of 128 x 64, two on a SIMD, which take turns: while one issues 32 MFMAs (half
@@ -394,17 +409,21 @@ struct BigTile {
     static constexpr int NTHREADS = 512, BM = 256, BN = 256, MSUB = 8, NSUB = 4, STAGE = (BM + BN) * 128, LDS = 2 * STAGE;
 };
 
-template <Product P>
-__global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(OrthoGemm p) {
+// SPLIT: as small_tile's.
+template <Product P, bool SPLIT>
+__device__ __forceinline__ void large_tile(const OrthoGemm& p, v4f* parts, int split) {
     using C = BigTile;
     extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     int64_t batch;
     int ti, tj;
-    big_tile<P>(p, xcd_remap((int)blockIdx.x, (int)gridDim.x), batch, ti, tj);
-    const int m0 = ti * C::BM, n0 = tj * C::BN, nkb = p.ld / BK;
-    const uint8_t *pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld), *qp = q_first<P>(p, batch, n0);
+    const int id = xcd_remap((int)blockIdx.x, (int)gridDim.x), all = SPLIT ? (int)gridDim.x / split : 0, part = SPLIT ? id / all : 0;
+    big_tile<P>(p, SPLIT ? id - part * all : id, batch, ti, tj);
+    const int steps = p.ld / BK, k0 = SPLIT ? part * steps / split : 0, nkb = SPLIT ? (part + 1) * steps / split - k0 : steps;
+    const int m0 = ti * C::BM, n0 = tj * C::BN;
+    const uint8_t* pp = (const uint8_t*)(p.p + batch * p.p_batch + (int64_t)m0 * p.ld) + k0 * 128;
+    const uint8_t* qp = q_first<P>(p, batch, n0) + k0 * q_step<P>(p);
 
     // Loads: an instruction fills 8 rows of 128 bytes. A0 is rows [0, 64) and [128, 192) of the tile; a wave loads 16 rows of
     // each half and four parts of B.
@@ -499,11 +518,22 @@ __global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(Orth
     }
     if (wm == 0) __builtin_amdgcn_s_barrier();           // every wave passes the same number of barriers
     __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();                                     // the stages are free
-    uint2 e[C::MSUB][C::NSUB];
-    load_e<P>(p, e, batch, m0, n0, wm * 128, wn * 64);
-    finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 128, wn * 64, symmetric(P) && ti == tj);
+    if constexpr (SPLIT) {                               // a wave's 128 x 64
+#pragma unroll
+        for (int i = 0; i < C::MSUB; i++) {
+            v4f* to = parts + ((int64_t)id * 16 + (2 * wm + i / 4) * 4 + wn) * 1024 + i % 4 * (C::NSUB * 64) + lane;
+#pragma unroll
+            for (int j = 0; j < C::NSUB; j++) to[j * 64] = acc[i][j];
+        }
+    } else {
+        __syncthreads();                                 // the stages are free
+        uint2 e[C::MSUB][C::NSUB];
+        load_e<P>(p, e, batch, m0, n0, wm * 128, wn * 64);
+        finish<P, C::BM, C::BN, C::NTHREADS>(p, acc, e, smem, batch, m0, n0, wm * 128, wn * 64, symmetric(P) && ti == tj);
+    }
 }
+template <Product P>
+__global__ __launch_bounds__(BigTile::NTHREADS, 1) void fg_ortho_big_kernel(OrthoGemm p) { large_tile<P, false>(p, nullptr, 1); }
 
 // ------------------------------------------------------------------------------------------------
 // 64 x 64 workgroup tiles for small matrices: 4 waves, each with a quarter of the contraction (every fourth K step) for the whole
@@ -519,7 +549,8 @@ struct SmallTile {
     static constexpr int LDS = SLOTS == 2 ? WAVES * 2 * STAGE : WAVES * STAGE + 8192;
 };
 
-// SPLIT: the contraction's part number id / (tiles of all matrices) of `split`; its sums go to `parts`.
+// SPLIT: the contraction's part number id / (tiles of all matrices) of `split`. Its sums go to `parts`: [part][64 x 64 tile][16 x 16
+// tile][lane], those of a larger tile row by row.
 template <Product P, int SLOTS, bool SPLIT>
 __device__ __forceinline__ void small_tile(const OrthoGemm& p, v4f* parts, int split) {
     using C = SmallTile<SLOTS>;
@@ -605,10 +636,10 @@ __device__ __forceinline__ void small_tile(const OrthoGemm& p, v4f* parts, int s
 #pragma unroll
         for (int w = 1; w < C::WAVES; w++) sum[0][j] += red[((w * C::SUB + wave) * C::SUB + j) * 64 + lane];
     }
-    if constexpr (SPLIT) {                               // rows of 64, a wave's 16
-        v4f* to = parts + (int64_t)id * (C::SIDE * C::SIDE / 4) + (16 * wave + lrow) * (C::SIDE / 4) + g16;
+    if constexpr (SPLIT) {
+        v4f* to = parts + (int64_t)id * 1024 + wave * (C::SUB * 64) + lane;
 #pragma unroll
-        for (int j = 0; j < C::SUB; j++) to[4 * j] = sum[0][j];
+        for (int j = 0; j < C::SUB; j++) to[j * 64] = sum[0][j];
     } else {
         finish<P, C::SIDE, C::SIDE, C::NTHREADS>(p, sum, e, smem + C::WAVES * 16384, batch, m0, n0, 16 * wave, 0, symmetric(P) && ti == tj);
     }
@@ -616,29 +647,43 @@ __device__ __forceinline__ void small_tile(const OrthoGemm& p, v4f* parts, int s
 template <Product P, int SLOTS>
 __global__ __launch_bounds__(256, 3 - SLOTS) void fg_ortho_small_kernel(OrthoGemm p) { small_tile<P, SLOTS, false>(p, nullptr, 1); }
 
-// A of few rows and a long contraction: 64 x 64 tiles that several workgroups share, as many as there are CUs. 64 x 16384, one tile
+// A of few tiles and a long contraction: tiles that several workgroups share, as many as there are CUs. 64 x 16384, one tile of 64 x 64
 // and 256 K steps: 5.8 us and 3.4 for the sum of 32 parts; with one workgroup 34 us.
+// 1536 x 16384 on tiles of 128, three parts each, 60 us instead of 108; 2048 x 16384 on tiles of 256, seven parts, 90 instead of 133.
 __global__ __launch_bounds__(256, 1) void fg_ortho_split_kernel(OrthoGemm p, v4f* parts, int split) {
     small_tile<PRODUCT_A, 2, true>(p, parts, split);
 }
-// The sum of the parts, in their order, and its end: 16 rows of a tile a workgroup, four columns a thread.
-__global__ __launch_bounds__(256) void fg_ortho_join_kernel(OrthoGemm p, const v4f* __restrict__ parts, int split) {
+__global__ __launch_bounds__(256, 1) void fg_ortho_mid_split_kernel(OrthoGemm p, v4f* parts, int split) {
+    mid_tile<PRODUCT_A, 4, true>(p, parts, split);
+}
+__global__ __launch_bounds__(512, 1) void fg_ortho_big_split_kernel(OrthoGemm p, v4f* parts, int split) {
+    large_tile<PRODUCT_A, true>(p, parts, split);
+}
+// The sum of the parts, in their order, and its end: 16 rows of a 64 x 64 tile a workgroup, four columns a thread. `side`: 64 x 64
+// tiles to a side of the split ones, 1, 2 or 4.
+__global__ __launch_bounds__(256) void fg_ortho_join_kernel(OrthoGemm p, const v4f* __restrict__ parts, int split, int side) {
     __shared__ __attribute__((aligned(16))) uint16_t turned[64][20];     // [column][row]
-    const int tid = threadIdx.x, all = (int)gridDim.x >> 2, strip = blockIdx.x & 3, r = tid >> 4, c = 4 * (tid & 15);
+    const int tid = threadIdx.x, lane = tid & 63, tile = blockIdx.x >> 2, strip = blockIdx.x & 3;
+    const int r = lane & 15, c = 16 * (tid >> 6) + 4 * (lane >> 4);
     int64_t batch;
     int ti, tj;
-    plain_tile<PRODUCT_A>(p, blockIdx.x >> 2, batch, ti, tj);
-    const v4f* from = parts + (int64_t)(blockIdx.x >> 2) * 1024 + strip * 256 + tid;
+    const int whole = tile / (side * side), within = tile - whole * side * side;
+    plain_tile<PRODUCT_A>(p, whole, batch, ti, tj);
+    ti = side * ti + within / side;
+    tj = side * tj + within % side;
+    if (ti * 64 >= p.M || tj > ti) return;               // nothing, or what the tile across the diagonal writes
+    const v4f* from = parts + (int64_t)tile * 1024 + strip * 256 + tid;
+    const int64_t next = (int64_t)(gridDim.x >> 2) * 1024;
     v4f sum = {0.f, 0.f, 0.f, 0.f};
     int part = 0;
     for (; part + 8 <= split; part += 8) {
         v4f v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) v[i] = from[(int64_t)(part + i) * all * 1024];
+        for (int i = 0; i < 8; i++) v[i] = from[(part + i) * next];
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += v[i];
     }
-    for (; part < split; part++) sum += from[(int64_t)part * all * 1024];
+    for (; part < split; part++) sum += from[part * next];
     const int m = ti * 64 + strip * 16 + r, n = tj * 64 + c;
     uint32_t h[4];
 #pragma unroll
@@ -802,15 +847,19 @@ template <Product P>
 hipError_t launch_gemm(const OrthoGemm& p, int64_t batch, hipStream_t stream, void* parts = nullptr, int64_t parts_bytes = 0) {
     const int64_t cus = fg_device_cus();
     if constexpr (P == PRODUCT_A) {
-        const int64_t tiles = ortho_tiles(batch, p.M, p.N, true, 64);
-        const int64_t split = ortho_split(tiles, p.ld / BK, parts_bytes / (tiles * 64 * 64 * 4), cus);
-        if (split > 1) {
+        const OrthoSplit split = ortho_split(batch, p.M, p.ld / BK, parts_bytes, cus);
+        if (split.parts > 1) {
+            const int64_t tiles = ortho_tiles(batch, p.M, p.N, true, (int)split.side);
+            const int size = split.side == 64 ? 0 : split.side == 128 ? 1 : 2, side = 1 << size;
+            const auto kern = size == 0 ? fg_ortho_split_kernel : size == 1 ? fg_ortho_mid_split_kernel : fg_ortho_big_split_kernel;
+            const int lds = size == 0 ? SmallTile<2>::LDS : size == 1 ? 4 * MidTile::STAGE : BigTile::LDS;
             OrthoGemm g = p;
             g.tiles = (int)(tiles / batch);
-            static std::atomic<uint64_t> limit;
-            if (const hipError_t e = fg_set_lds_limit_once((const void*)fg_ortho_split_kernel, SmallTile<2>::LDS, limit); e != hipSuccess) return e;
-            hipLaunchKernelGGL(fg_ortho_split_kernel, dim3((unsigned)(tiles * split)), dim3(256), SmallTile<2>::LDS, stream, g, (v4f*)parts, (int)split);
-            hipLaunchKernelGGL(fg_ortho_join_kernel, dim3((unsigned)(4 * tiles)), dim3(256), 0, stream, g, (const v4f*)parts, (int)split);
+            static std::atomic<uint64_t> limits[3];
+            if (const hipError_t e = fg_set_lds_limit_once((const void*)kern, lds, limits[size]); e != hipSuccess) return e;
+            hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * split.parts)), dim3(size == 2 ? 512 : 256), lds, stream, g, (v4f*)parts, (int)split.parts);
+            hipLaunchKernelGGL(fg_ortho_join_kernel, dim3((unsigned)(tiles * side * side * 4)), dim3(256), 0, stream, g, (const v4f*)parts,
+                               (int)split.parts, side);
             return hipGetLastError();
         }
     }

@@ -51,19 +51,7 @@ inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_
 // (The quarters' contraction split in two, with a third launch for the sums: 64 us instead of 72, and 38 instead of 29.)
 inline OrthoTile ortho_tail_tile(int64_t rest, int64_t cus) { return 4 * rest <= cus ? TILE_128 : TILE_128_PAIRS; }
 
-// Workgroups that share the contraction of each of a symmetric product's 64 x 64 tiles where there are few tiles, with a second launch
-// that adds their sums; 1: none. `room`: parts of all tiles that the workspace has. The second launch costs about 4.5 us, as much
-// as 26 K steps. A whole update by m x n, with one workgroup a tile and with several: 64 x 2048 (32 steps, 4 parts) 87 and 91 us,
-// 256 x 2048 (4) 105 and 104, 64 x 4096 (8) 106 and 90, 64 x 16384 (32) 221 and 95, 512 x 4096 (7) 152 and 141, two of 496 x 3973
-// (3) 174 and 169, 640 x 10240 (4) 292 and 199, 856 x 11323 (2) 382 and 318.
-inline int64_t ortho_split(int64_t tiles, int64_t steps, int64_t room, int64_t cus) {
-    int64_t split = cus / tiles;
-    if (split > steps / 8) split = steps / 8;
-    if (split > room) split = room;
-    return split > 1 && steps - steps / split >= 40 ? split : 1;
-}
-
-inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus) {
+inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus, double* estimate = nullptr) {
     const OrthoTile shapes[] = {TILE_64, TILE_128, TILE_128_PAIRS, TILE_256};
     const int sides[] = {64, 128, 128, 256};
     OrthoTile best = TILE_64;
@@ -75,7 +63,33 @@ inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric,
     const int64_t big = ortho_tiles(batch, M, N, symmetric, 256), rest = big % cus;
     if (big > cus && rest > 0) {
         const double us = ortho_tile_us(TILE_256, big - rest, steps, cus) + ortho_tile_us(ortho_tail_tile(rest, cus), 4 * rest, steps, cus);
-        if (us < least) best = TILE_256_TAIL;
+        if (us < least) best = TILE_256_TAIL, least = us;
+    }
+    if (estimate) *estimate = least;
+    return best;
+}
+
+// A symmetric product's tiles of `side` whose contraction `parts` workgroups share each, with a second launch that adds their sums;
+// parts 1: none. As many parts as CUs, a part of at least eight steps, and `room` bytes for the sums.
+struct OrthoSplit {
+    int64_t side, parts;
+};
+// The second launch takes 4.5 us and the sums' way to memory and back. Whole updates by m x n, with one workgroup a tile and with several:
+// 64 x 2048 87 and 91 us, 256 x 2048 105 and 100, 64 x 4096 106 and 84, 64 x 16384 221 and 92, 512 x 4096 152 and 139, two of 496 x
+// 3973 174 and 167, 640 x 10240 291 and 194; on tiles of 128 1024 x 4096 191 and 217, 1024 x 16384 446 and 387, 1536 x 8192 530 and 445;
+// on tiles of 256 2560 x 8192 967 and 1029, 2048 x 16384 1321 and 1106, 3000 x 18432 2721 and 2416.
+inline OrthoSplit ortho_split(int64_t batch, int64_t M, int64_t steps, int64_t room, int64_t cus) {
+    double least;
+    ortho_tile(batch, M, M, true, steps, cus, &least);
+    OrthoSplit best = {64, 1};
+    for (int64_t side = 64; side <= 256; side *= 2) {
+        const int64_t tiles = ortho_tiles(batch, M, M, true, (int)side), bytes = tiles * side * side * 4;
+        int64_t parts = cus / tiles;
+        if (parts > steps / 8) parts = steps / 8;
+        if (parts > room / bytes) parts = room / bytes;
+        if (parts < 2) continue;
+        const double us = ortho_tile_us(side == 64 ? TILE_64 : side == 128 ? TILE_128 : TILE_256, tiles * parts, (steps + parts - 1) / parts, cus) + 4.5 + (double)(2 * parts * bytes) / 4.7e6;
+        if (us < least) best = {side, parts}, least = us;
     }
     return best;
 }

@@ -361,7 +361,8 @@ def test_update_in_place(shape):
 
 
 @pytest.mark.parametrize("batch,n,k", [(1, 64, 8192), (2, 76, 16200), (3, 5000, 130), (1, 33, 3003), (4, 60, 4200), (1, 309, 4853), (1, 700, 8192),
-                                       (2, 3973, 496), (1, 856, 11323)])
+                                       (2, 3973, 496), (1, 856, 11323), (1, 1024, 16384), (1, 8200, 1500), (2, 1024, 8192),
+                                       (1, 2048, 16384), (1, 2000, 18000), (2, 2048, 8192)])
 def test_update_of_few_rows(batch, n, k):
     """Long contractions that several workgroups share, as far as the workspace has room for their sums."""
     g = torch.stack([gradient(i, n, k) for i in range(batch)])

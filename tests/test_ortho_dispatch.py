@@ -30,16 +30,16 @@ def ask(tmp_path_factory):
     assert r.returncode == 0, r.stderr
 
     def run(problems):
-        text = "".join(" ".join(map(str, p)) + "\n" for p in problems)
+        text = "".join(" ".join(map(str, [*p, 0][:6])) + "\n" for p in problems)
         r = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=60, env=dict(os.environ, ASAN_OPTIONS="verify_asan_link_order=0"))
         assert r.returncode == 0 and "runtime error" not in r.stderr, r.stderr
         lines = [line.split() for line in r.stdout.splitlines()]
-        return [(int(v[0]), [float(x) for x in v[1:]]) for v in lines]
+        return [(int(v[0]), [float(x) for x in v[3:]], (int(v[1]), int(v[2]))) for v in lines]
     return run
 
 
 def test_estimates_and_choices(ask):
-    for (problem, measured), (choice, us) in zip(MEASURED.items(), ask(list(MEASURED))):
+    for (problem, measured), (choice, us, _) in zip(MEASURED.items(), ask(list(MEASURED))):
         for m, e in zip(measured, us):
             assert m is None or 0.65 < e / m < 1.5, (problem, measured, us)
         fastest = min(m for m in measured if m is not None)
@@ -48,20 +48,38 @@ def test_estimates_and_choices(ask):
 
 def test_rest_of_a_round(ask):
     # 288 tiles of 256: one round, and 32 tiles in quarters; 256 and 136 tiles have no whole round with a rest
-    (tail, _), (even, _), (few, _) = ask([(8, 2048, 2048, 1, 112), (1, 4096, 4096, 0, 64), (1, 4096, 4096, 1, 64)])
+    (tail, *_), (even, *_), (few, *_) = ask([(8, 2048, 2048, 1, 112), (1, 4096, 4096, 0, 64), (1, 4096, 4096, 1, 64)])
     assert (tail, even, few) == (4, 3, 3)
 
 
-def test_split_contractions(ask):
-    # tiles and steps: (1, 256), (3, 64), (10, 32), (36, 64), (55, 160), (105, 177), (136, 256)
-    problems = [(1, 64, 64, 1, 256), (1, 128, 128, 1, 64), (1, 256, 256, 1, 32), (1, 512, 512, 1, 64), (1, 640, 640, 1, 160), (1, 856, 856, 1, 177),
-                (1, 1024, 1024, 1, 256)]
-    assert [int(us[4]) for _, us in ask(problems)] == [32, 8, 1, 7, 4, 2, 1]
+# Whole updates (us, five steps; batch, m, n) whose A has one workgroup a tile, and several on tiles of 64, 128 and 256
+SPLITS = {(1, 64, 4096): (106, 84, 98, None), (1, 64, 16384): (221, 92, 108, None), (2, 76, 16200): (245, 135, 161, None),
+          (1, 256, 2048): (105, 100, 114, None), (1, 256, 8192): (188, 110, 126, None), (1, 309, 4853): (160, 120, 144, None),
+          (1, 512, 4096): (152, 139, 155, None), (1, 512, 16384): (317, 190, 208, None), (2, 496, 3973): (174, 167, 204, None),
+          (1, 640, 10240): (291, 194, 223, None), (1, 768, 16384): (384, 286, 292, None), (1, 856, 11323): (376, 311, 310, None),
+          (1, 1024, 4096): (191, None, 217, None), (1, 1024, 16384): (446, None, 387, 407), (1, 1280, 16384): (599, None, 577, 563),
+          (1, 1536, 4096): (328, None, 329, None), (1, 1536, 8192): (530, None, 445, 484), (1, 1536, 16384): (996, None, 755, 724),
+          (1, 1900, 18432): (1536, None, 1264, 1179), (1, 2048, 4096): (470, None, None, 470), (1, 2048, 8192): (725, None, None, 706),
+          (1, 2048, 16384): (1321, None, None, 1106), (1, 2560, 2560): (476, None, None, 475), (1, 2560, 8192): (967, None, None, 1029),
+          (1, 3000, 18432): (2721, None, None, 2416), (2, 1024, 8192): (458, None, 414, 428), (2, 2048, 8192): (1305, None, None, 1172),
+          (4, 512, 8192): (281, None, 287, None), (4, 1024, 4096): (439, None, 438, 457)}
+
+
+def test_shared_contractions(ask):
+    def problem(b, m, n):
+        return b, m, m, 1, (n + 63) // 64, 2 * (b if m % 64 == 0 else 1) * m * ((n + 63) // 64 * 64)
+    for (size, measured), (_, _, (side, parts)) in zip(SPLITS.items(), ask([problem(*k) for k in SPLITS])):
+        us = measured[{0: 0, 64: 1, 128: 2, 256: 3}[side]]
+        assert (side == 0) == (parts == 1) and us is not None and us <= 1.08 * min(m for m in measured if m), (size, side, parts)
+    # no part of fewer than eight steps, no more parts than the room holds or the CUs take
+    for b, m, n, room in ((1, 64, 16384, 16384 * 3), (1, 64, 16384, 16383), (1, 64, 1000, 1 << 40), (300, 64, 16384, 1 << 40)):
+        (_, _, (side, parts)), = ask([(b, m, m, 1, (n + 63) // 64, room)])
+        assert parts <= max(1, min(room // 16384, (n + 63) // 512, 256 // b)), (b, m, n, room, parts)
 
 
 def test_every_size_has_a_choice(ask):
     sides = (1, 2, 63, 64, 65, 129, 500, 1000, 3000, 8191, 20000, 65536)
     problems = [(b, m, n, int(m == n), (n + 63) // 64) for b in (1, 7, 300, 65535) for m in sides for n in sides
                 if m <= n and b * ((m + 63) // 64) * ((n + 63) // 64) < 1 << 24]
-    for problem, (choice, us) in zip(problems, ask(problems)):
-        assert 0 <= choice <= 4 and all(u > 0 for u in us) and us[4] <= 256, problem
+    for problem, (choice, us, (_, parts)) in zip(problems, ask([(*p, 1 << 40) for p in problems])):
+        assert 0 <= choice <= 4 and all(u > 0 for u in us) and 1 <= parts <= 256, problem
