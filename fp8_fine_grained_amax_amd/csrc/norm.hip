@@ -735,7 +735,11 @@ hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
             });
         }
         const int u = (int)std::min<int64_t>(units, units <= 32 ? 2 : 3), waves = (int)((units + u - 1) / u), groups = std::max(1, 4 / waves);
-        const int64_t fill = cus * std::max(1, 16 / (waves * groups));
+        // Waves of a CU: a bf16 row's need half the bytes, so more of them are in flight. 16 and 24: bf16 6000 x 5632 34.7 and 28.2 us, 4096
+        // x 12288 41.8 and 36.7, 4096 x 7168 both 22, but 16384 x 2048 21.5 and 23.0 and three groups (4096 x 18432) 49.1 and 51.4; f32 6000
+        // x 5632 36.1 and 38.7; the statistics alone 4096 x 18432 f32 145 and 146.
+        const int resident = TILES && p.x_bf16 && u == 2 && p.cols > 2048 ? 24 : 16;
+        const int64_t fill = cus * std::max(1, resident / (waves * groups));
         switch (u) {
             case 1: return launch_fwd<1, false, TILES>(p, waves, groups, fill, stream);
             case 2: return launch_fwd<2, false, TILES>(p, waves, groups, fill, stream);
