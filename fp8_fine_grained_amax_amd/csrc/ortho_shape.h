@@ -48,7 +48,8 @@ inline double ortho_tile_us(OrthoTile tile, int64_t tiles, int64_t steps, int64_
 
 // The rest of whole rounds of 256 x 256 tiles, in quarters on 128 x 128 tiles, one or two to a CU. Eight symmetric 2048 x 2048
 // (288 tiles), 112 steps: 267 us in two launches and 299 in one; 32 steps: 103 and 111 (102 on 128 x 128 tiles alone).
-// (The quarters' contraction split in two, with a third launch for the sums: 64 us instead of 72, and 38 instead of 29.)
+// (Several workgroups to a tile of the rest, as below, took 49 us instead of 68 to 74 in quarters with 112 steps, 28 and 22 with 32;
+// but the matrices of a batch would then have their sums in different orders.)
 inline OrthoTile ortho_tail_tile(int64_t rest, int64_t cus) { return 4 * rest <= cus ? TILE_128 : TILE_128_PAIRS; }
 
 inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric, int64_t steps, int64_t cus, double* estimate = nullptr) {
@@ -74,7 +75,7 @@ inline OrthoTile ortho_tile(int64_t batch, int64_t M, int64_t N, bool symmetric,
 struct OrthoSplit {
     int64_t side, parts;
 };
-// The second launch takes 4.5 us and the sums' way to memory and back. Whole updates by m x n, with one workgroup a tile and with several:
+// The second launch and the sums' way to the Infinity Cache and back: 4.5 us and 14 for 64 MB. Whole updates by m x n, with one workgroup a tile and with several:
 // 64 x 2048 87 and 91 us, 256 x 2048 105 and 100, 64 x 4096 106 and 84, 64 x 16384 221 and 92, 512 x 4096 152 and 139, two of 496 x
 // 3973 174 and 167, 640 x 10240 291 and 194; on tiles of 128 1024 x 4096 191 and 217, 1024 x 16384 446 and 387, 1536 x 8192 530 and 445;
 // on tiles of 256 2560 x 8192 967 and 1029, 2048 x 16384 1321 and 1106, 3000 x 18432 2721 and 2416.
@@ -88,7 +89,7 @@ inline OrthoSplit ortho_split(int64_t batch, int64_t M, int64_t steps, int64_t r
         if (parts > steps / 8) parts = steps / 8;
         if (parts > room / bytes) parts = room / bytes;
         if (parts < 2) continue;
-        const double us = ortho_tile_us(side == 64 ? TILE_64 : side == 128 ? TILE_128 : TILE_256, tiles * parts, (steps + parts - 1) / parts, cus) + 4.5 + (double)(2 * parts * bytes) / 4.7e6;
+        const double us = ortho_tile_us(side == 64 ? TILE_64 : side == 128 ? TILE_128 : TILE_256, tiles * parts, (steps + parts - 1) / parts, cus) + 4.5 + (double)(parts * bytes) / 4.7e6;
         if (us < least) best = {side, parts}, least = us;
     }
     return best;

@@ -339,7 +339,7 @@ def test_update_batches_and_strides(shape):
 
 @pytest.mark.parametrize("batch,n,k,steps", [(1, 1100, 4200, 2), (1, 2040, 2100, 1), (3, 1030, 2100, 2), (1, 4096, 4160, 1), (8, 2048, 2048, 2), (9, 2050, 1990, 1),
                                                (1, 2048, 8448, 2), (1, 2000, 8400, 2), (8, 2000, 2040, 1), (8, 512, 1024, 2), (8, 1024, 2050, 2),
-                                               (1, 2000, 10400, 2)])
+                                               (1, 2000, 10400, 2), (8, 2048, 7168, 1), (8, 2000, 7000, 1)])
 def test_update_on_every_tile(batch, n, k, steps):
     """Sizes whose products take the 128 x 128 tiles in both forms, the 256 x 256 ones, and those with a rest in quarters, whose
     matrices are the last."""
