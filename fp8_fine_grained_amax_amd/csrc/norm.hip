@@ -739,7 +739,9 @@ hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
         // x 12288 41.8 and 36.7, 4096 x 7168 both 22, but 16384 x 2048 21.5 and 23.0 and three groups (4096 x 18432) 49.1 and 51.4; f32 6000
         // x 5632 36.1 and 38.7; the statistics alone 4096 x 18432 f32 145 and 146.
         const int resident = TILES && p.x_bf16 && u == 2 && p.cols > 2048 ? 24 : 16;
-        const int64_t fill = cus * std::max(1, resident / (waves * groups));
+        // no more workgroups than a CU's 160 KB hold the weights of: with beta, 4096 x 7168 26.5 us, with three of them, of which two fit, 31
+        const int64_t held = TILES ? (160 * 1024) / (p.cols * (p.beta ? 8 : 4) + 512) : 16;
+        const int64_t fill = cus * std::max<int64_t>(1, std::min<int64_t>(resident / (waves * groups), held));
         switch (u) {
             case 1: return launch_fwd<1, false, TILES>(p, waves, groups, fill, stream);
             case 2: return launch_fwd<2, false, TILES>(p, waves, groups, fill, stream);
