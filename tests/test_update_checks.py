@@ -39,3 +39,26 @@ def test_limits_of_a_gradient(n, k):
     if min(n, k) > 4:
         wrong["bf16"] = ref.emulate(g, kept=torch.bfloat16)
     assert [name for name, out in wrong.items() if passes(out, limits)] == []
+
+
+@pytest.mark.parametrize("n,k", [(40, 60), (300, 900), (1000, 640)])
+@pytest.mark.parametrize("name", ref.PRODUCTS)
+def test_limits_of_a_product(n, k, name):
+    """A product that is missing, has the wrong sign, is 2% off, misses a K step, or has one tile of zeros."""
+    coefficients, steps, _ = ref.PRODUCTS[name]
+    g, u, v = ref.of_rank(3, n, k, [1.0] * ref.RANK)
+    how = dict(steps=steps, coefficients=coefficients, scale=ref.product_scale(name))
+    limits = ref.product_limits(name, u, v)
+    want = limits[0]
+    for fp32 in (False, True):
+        assert passes(ref.emulate(g, fp32=fp32, **how), limits)
+    tile = want.clone()
+    tile[-30:, -30:] = 0
+    short = (u if n <= k else v).clone()        # of A = X X^T, the smaller side's
+    long = v if n <= k else u
+    lost = long[64:].t() @ long[64:] if max(n, k) > 64 else torch.zeros(8, 8, dtype=torch.float64)
+    wrong = dict(zeros=0 * want, negated=-want, larger=1.02 * want, tile=tile)
+    if name == "A X":
+        x = short @ lost @ long.t()
+        wrong["lost"] = x if n <= k else x.t()
+    assert [w for w, out in wrong.items() if passes(out, limits)] == []

@@ -71,3 +71,36 @@ def check(out, want, limit, element, what=""):
     assert bool(torch.isfinite(out).all()), what
     assert float(off.norm()) <= 1.02 * limit, (what, float(off.norm() / want.norm()), limit / float(want.norm()))
     assert bool((off <= element).all()), (what, float((off - element).max()))
+
+
+def of_rank(seed, n, k, singular, dtype=torch.float64, device="cpu"):
+    """(matrix, U, V) with these singular values and random directions."""
+    gen = torch.Generator().manual_seed(seed)
+    r = len(singular)
+    u, v = (torch.linalg.qr(torch.randn(d, r, generator=gen, dtype=torch.float64))[0].to(device) for d in (n, k))
+    s = torch.as_tensor(singular, dtype=torch.float64, device=device)
+    return ((u * s) @ v.t()).to(dtype), u, v
+
+
+# A step of one term: coefficients, steps, and the number of half steps (2^-11) that fp16 takes of the result, to first order: X as
+# often as it is a factor, A as often as it is, and B; with two steps the X between them too.
+PRODUCTS = {"X": ((1.0, 0.0, 0.0), 1, 2), "X twice": ((1.25, 0.0, 0.0), 2, 4), "A X": ((0.0, 2.0, 0.0), 1, 5), "A A X": ((0.0, 0.0, 2.0), 1, 8)}
+RANK = 8
+
+
+def product_scale(name):
+    """What makes the result of a matrix of RANK equal directions U V^T."""
+    coefficients, steps, _ = PRODUCTS[name]
+    value = RANK ** -0.5
+    for _ in range(steps):
+        value = sum(c * value ** e for c, e in zip(coefficients, (1, 3, 5)))
+    return 1 / value
+
+
+def product_limits(name, u, v):
+    """As `limits`, for the result U V^T. Half a step of a factor's every element changes an element (i, j) of the result by no more than
+    half a step of |U_i| |V_j|."""
+    want = u @ v.t()
+    store, off = (want.to(torch.bfloat16).double() - want).norm(), PRODUCTS[name][2] * 2.0 ** -11
+    element = 1.02 * (want.abs() * 2.0 ** -8 + off * u.norm(dim=1)[:, None] * v.norm(dim=1)[None])
+    return want, float((store.square() + RANK * off ** 2).sqrt()), element
