@@ -1,5 +1,5 @@
-"""The orthogonalised update on the GPU within limits that follow from its fp16 roundings (update_ref.py): whole updates, and each
-product of a step by itself on every tile."""
+"""The orthogonalised update on the GPU within limits that follow from its fp16 roundings (update_ref.py): whole updates, each product
+of a step by itself on every tile, and spectra other than that of independent tokens."""
 import pytest
 import torch
 
@@ -59,3 +59,57 @@ def test_products(batch, n, k, name):
     out = update(torch.stack([m[0] for m in made]), steps=steps, coefficients=coefficients, scale=ref.product_scale(name))
     for i in {0, batch // 2, batch - 1}:
         ref.check(out[i], *ref.product_limits(name, *made[i][1:]), (batch, n, k, i))
+
+
+# ---- spectra --------------------------------------------------------------------------------------------
+
+def spectrum(name, m):
+    i = torch.arange(1, m + 1, dtype=torch.float64)
+    return {"1/sqrt i": i ** -0.5, "1/i": 1 / i, "1/i^2": i ** -2, "exp(-i/20)": torch.exp(-i / 20), "exp(-i/100)": torch.exp(-i / 100),
+            "flat": torch.ones_like(i)}[name]
+
+
+# what the header states of the update before it is rounded to bf16
+SPECTRA = {"flat": 2e-3, "1/sqrt i": 2e-3, "1/i": 4.5e-3, "1/i^2": 2.5e-2, "exp(-i/20)": 1.5e-2, "exp(-i/100)": 6.5e-3}
+
+
+@pytest.mark.parametrize("name", SPECTRA)
+@pytest.mark.parametrize("n,k", [(128, 512), (512, 1024), (2048, 1024)])
+def test_spectra(name, n, k):
+    g = ref.of_rank(5, n, k, spectrum(name, min(n, k)), torch.float32, device())[0]
+    limits = ref.limits(g.double())
+    out = update(g)
+    ref.check(out, *limits, name)
+    want = limits[0]
+    assert float((out.double() - want).norm() / want.norm()) <= (SPECTRA[name] ** 2 + 2e-3 ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("rank,stated", [(1, 0.15), (4, 0.08), (16, 0.05), (64, 0.03), (256, 0.009)])
+def test_few_directions(rank, stated):
+    """Along its directions the update is p^5(s), and the raised roundings in its empty ones are as large as the header says, within
+    a tenth."""
+    n, k = 1000, 1400
+    g, u, v = ref.of_rank(7, n, k, [1.0] * rank, torch.float32, device())
+    out = update(g).double()
+    limits = ref.limits(g.double())
+    ref.check(out, *limits, rank)
+    want = limits[0]
+    assert float((out - want).norm() / want.norm()) <= 1.1 * stated + 2e-3
+    along = (u * (out @ v)).sum(0)                  # u^T out v of each direction
+    s = rank ** -0.5
+    for _ in range(5):
+        s = 3.4445 * s - 4.7750 * s ** 3 + 2.0315 * s ** 5
+    # X, A and B round each element by itself, which hardly moves a direction as a whole: what the header says of ordinary gradients
+    assert float((along - s).abs().max()) <= 1.6e-3, (along, s)
+
+
+@pytest.mark.parametrize("size,stated", [(1e-10, 2e-3), (1e-12, 2e-3), (1e-13, 3e-3), (1e-14, 3e-2)])
+def test_far_below_eps(size, stated):
+    """Gradients far smaller than eps (1e-7), whose X has entries that fp16 holds with fewer bits."""
+    g = gradient(5, 256, 1024)
+    g *= size / g.double().norm()
+    limits = ref.limits(g.double())
+    out = update(g)
+    ref.check(out, *limits, size)
+    want = limits[0]
+    assert float((out.double() - want).norm() / want.norm()) <= (stated ** 2 + 2e-3 ** 2) ** 0.5
