@@ -27,7 +27,8 @@ namespace {
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int BK = 64;                           // a K step: 128 bytes of a row
-constexpr float kScaleX = 4096.0f, kScaleA = 2048.0f;
+constexpr int kLogScaleX = 12;
+constexpr float kScaleX = 1 << kLogScaleX, kScaleA = 2048.0f;
 constexpr int kNormParts = 256;                  // partial sums of a matrix's squares, at most
 
 int64_t pad(int64_t v) { return (v + BK - 1) / BK * BK; }
@@ -783,15 +784,19 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
         if (r0 + r + k < p.N) v[k] = load_g(p, (batch * p.N + r0 + r + k) * p.ld + c0 + c, p.K - c0 - c, whole && c0 + c < p.K);
     }
     const double sum = block_sum<4>((int)threadIdx.x < parts ? partial[batch * kNormParts + threadIdx.x] : 0.0, red);
-    const float norm = (float)__builtin_sqrt(sum);
-    const float inv = norm < __builtin_inff() ? (float)(1.0 / (double)(norm + p.eps)) : __builtin_nanf("");
+    // |G| + eps in fp32, and in 64 bits where fp32 has too few bits for it or none: X = G 2^-e inv, whose parts are normal numbers
+    // whatever the two are (a factor of 1 / 2^-140 alone would be infinite, and 0 times it NaN).
+    const float norm = (float)__builtin_sqrt(sum), rounded = norm + p.eps;
+    const double divisor = rounded >= 0x1p-126f && rounded < __builtin_inff() ? (double)rounded : __builtin_sqrt(sum) + (double)p.eps;
+    const int e = __builtin_amdgcn_frexp_exp(divisor);
+    const float inv = norm < __builtin_inff() ? (float)(1.0 / __builtin_amdgcn_ldexp(divisor, -e)) : __builtin_nanf("");
     uint32_t h[4][4];
 #pragma unroll
     for (int k = 0; k < 4; k++)
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const bool there = r0 + r + k < p.N && c0 + c + j < p.K;     // a factor of NaN leaves the padding 0
-            h[k][j] = there ? half_bits<_Float16>(v[k][j] * inv * kScaleX) : 0;
+            h[k][j] = there ? half_bits<_Float16>(__builtin_amdgcn_ldexpf(v[k][j], kLogScaleX - e) * inv) : 0;
         }
     const int64_t m = WIDE ? p.N : p.K;
     x += batch * rows * ld;

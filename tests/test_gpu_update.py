@@ -113,3 +113,20 @@ def test_far_below_eps(size, stated):
     ref.check(out, *limits, size)
     want = limits[0]
     assert float((out.double() - want).norm() / want.norm()) <= (stated ** 2 + 2e-3 ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("eps", [1.5e-45, 1e-41, 2.9e-39, 3e-39, 1e-30])
+def test_zeros_of_any_eps(eps):
+    assert not update(torch.zeros(70, 90, device=device()), eps=eps).any()
+    assert not update(torch.zeros(90, 70, device=device(), dtype=torch.bfloat16), eps=eps).any()
+
+
+@pytest.mark.parametrize("size,eps", [(1e-40, 1e-43), (3e-39, 1e-45), (2e-38, 1e-41), (1e-41, 2e-38), (1e-37, 1e-37), (1e30, 1e-45), (3e38, 1e-7), (3e38, 3e38),
+                                      (1e38, 3.3e38)])
+@pytest.mark.parametrize("n,k", [(120, 200), (200, 120)])
+def test_ends_of_fp32(size, eps, n, k):
+    """|G| and eps whose sum is denormal or past fp32's range, although X is neither."""
+    g = gradient(6, n, k).double()
+    g = (g * (size / float(g.norm()))).float()
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    ref.check(update(g, eps=eps), *ref.limits(g.double(), eps=eps), (size, eps))
