@@ -27,8 +27,7 @@ namespace {
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int BK = 64;                           // a K step: 128 bytes of a row
-constexpr int kLogScaleX = 12;
-constexpr float kScaleX = 1 << kLogScaleX, kScaleA = 2048.0f;
+constexpr float kScaleX = 4096.0f, kScaleA = 2048.0f;
 constexpr int kNormParts = 256;                  // partial sums of a matrix's squares, at most
 
 int64_t pad(int64_t v) { return (v + BK - 1) / BK * BK; }
@@ -796,7 +795,7 @@ __global__ __launch_bounds__(256) void fg_ortho_start_kernel(FgOrtho p, const do
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const bool there = r0 + r + k < p.N && c0 + c + j < p.K;     // a factor of NaN leaves the padding 0
-            h[k][j] = there ? half_bits<_Float16>(__builtin_amdgcn_ldexpf(v[k][j], kLogScaleX - e) * inv) : 0;
+            h[k][j] = there ? half_bits<_Float16>(__builtin_amdgcn_ldexpf(v[k][j], -e) * inv * kScaleX) : 0;
         }
     const int64_t m = WIDE ? p.N : p.K;
     x += batch * rows * ld;
