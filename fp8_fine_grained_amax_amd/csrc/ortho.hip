@@ -39,7 +39,7 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 enum Product { PRODUCT_A, PRODUCT_B, PRODUCT_X, PRODUCT_LAST };
 constexpr bool symmetric(Product P) { return P == PRODUCT_A || P == PRODUCT_B; }
 
-// C = alpha P Q^T of every matrix of a batch; in B, where Q is P, beta P + diag I beside it. A launch begins with the arguments' way
+// C = alpha P Q^T of every matrix of a batch; in B, where Q is P, beta P + diag I beside it, and in the last product times beta. A launch begins with the arguments' way
 // from the host's memory: 168 bytes of them instead of 104 cost a small product 0.1 to 0.2 us.
 struct OrthoGemm {
     const uint16_t *p, *q;                       // fp16 [M][ld]; of A and B [N][ld], of X [ld][ld_q]
@@ -211,6 +211,7 @@ __device__ __forceinline__ void finish(const OrthoGemm& p, const v4f (&acc)[MSUB
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 v[k] = p.alpha * acc[i][j][k];
+                if constexpr (LAST) v[k] *= p.beta;            // the caller's factor: times alpha it may be denormal
                 if constexpr (P == PRODUCT_B) {
                     const uint32_t h = k & 2 ? w[i][j].y : w[i][j].x;
                     const float old = (float)__builtin_bit_cast(_Float16, (unsigned short)(k & 1 ? h >> 16 : h));
@@ -935,7 +936,7 @@ hipError_t fg_launch_orthogonalize(const FgOrtho& o, hipStream_t stream) {
         } else {
             g.out = o.out; g.ld_out = (int)o.K; g.out_batch = o.N * o.K;
             g.turned = !wide;
-            g.alpha = o.scale / (kScaleA * kScaleX);
+            g.alpha = 1.0f / (kScaleA * kScaleX); g.beta = o.scale;
             if (const hipError_t e = launch_gemm<PRODUCT_LAST>(g, o.batch, stream); e != hipSuccess) return e;
         }
         std::swap(x, next);

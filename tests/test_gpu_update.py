@@ -130,3 +130,20 @@ def test_ends_of_fp32(size, eps, n, k):
     g = (g * (size / float(g.norm()))).float()
     eps = float(torch.tensor(eps, dtype=torch.float32))
     ref.check(update(g, eps=eps), *ref.limits(g.double(), eps=eps), (size, eps))
+
+
+@pytest.mark.parametrize("scale", [1e-31, -1e-36, 1e-37, 3e-38, 1e38, -0.0])
+@pytest.mark.parametrize("n,k", [(8, 8), (500, 300), (1100, 4200), (2048, 8448)])
+def test_scales(n, k, scale):
+    """Factors whose product with X's and B's own scales is denormal, on each kind of tile: the same numbers times the factor, as
+    long as those are not denormal themselves. One direction of eight ones, so that they are 1 / 8 and 0."""
+    g = torch.zeros(n, k, device=device())
+    g[:8, :8] = 1
+    one = update(g, steps=1, coefficients=(1.0, 0.0, 0.0))
+    out = update(g, steps=1, coefficients=(1.0, 0.0, 0.0), scale=scale)
+    want = torch.zeros(n, k, dtype=torch.float64, device=device())
+    want[:8, :8] = 0.125
+    assert torch.equal(one.double(), want)
+    tiny = 2.0 ** -134 if abs(scale) < 1e-37 else 0.0           # half a step of a denormal bf16
+    factor = float(torch.tensor(scale, dtype=torch.float32))
+    assert bool(((out.double() - factor * want).abs() <= (factor * want).abs() * 2.0 ** -8 + tiny).all())
