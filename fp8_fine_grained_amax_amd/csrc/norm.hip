@@ -8,7 +8,8 @@
 // against 36.4, 4096 x 18432 f32 155 against 147.)
 //
 // y is (x gamma) rstd, in this order: the product of two bf16 numbers is exact in FP32, so RMS of bf16 x and gamma rounds once
-// before the codes, whose borders such products often lie on.
+// before the codes, whose borders such products often lie on. rstd's power of two goes to x first, which rounds nothing and keeps
+// x gamma from overflowing where y does not.
 #include "host_util.h"
 #include "tile8.h"
 #include "train_launch.h"
@@ -80,6 +81,27 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 __device__ __forceinline__ float wave_sum(float v) { return rows_sum(row16_sum(v)); }
+
+// y's parts: ((x - mean) power gamma) rest, where power rest is rstd, power a power of two, and rest in [1, 2), so that the first three
+// factors are as large as y at most. (x - mean) power is one operation, rounded as x - mean is, as long as mean power is in range: where it
+// would not be (a constant row and a tiny eps), power is less and rest more. A rstd of NaN makes rest NaN; zero or denormal it is not.
+template <bool LAYER>
+struct Normed {
+    float power, shift, rest;
+    __device__ __forceinline__ void set(float mean, float rstd) {
+        uint32_t e = __float_as_uint(rstd) >> 23 & 255;
+        if constexpr (LAYER) {
+            const uint32_t most = 380 - (__float_as_uint(mean) >> 23 & 255);       // the product below 2^128
+            e = e < most ? e : most;
+        }
+        power = __uint_as_float(e << 23);
+        shift = LAYER ? -mean * power : 0.0f;
+        rest = rstd * __uint_as_float((254 - e) << 23);
+    }
+    __device__ __forceinline__ float gained(float x, float gamma) const {
+        return (LAYER ? __builtin_fmaf(x, power, shift) : x * power) * gamma;
+    }
+};
 
 constexpr int kMaxWaves = 16;
 // Threads of a workgroup whose threads hold U groups of eight columns each: with more groups a thread needs more registers
@@ -230,6 +252,8 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
         }
         if constexpr (!TILES) continue;
         float top[U], s[U];
+        Normed<LAYER> normed;
+        normed.set(mean, rstd);
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int c = at.t + u * at.span;
@@ -247,13 +271,13 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; e++) v[u][e] = (LAYER ? v[u][e] - mean : v[u][e]) * gamma[FEW ? u : 0][e];
+            for (int e = 0; e < 8; e++) v[u][e] = normed.gained(v[u][e], gamma[FEW ? u : 0][e]);
             if (p.beta) {
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[u][e] = __builtin_fmaf(v[u][e], rstd, beta[FEW ? u : 0][e]);
+                for (int e = 0; e < 8; e++) v[u][e] = __builtin_fmaf(v[u][e], normed.rest, beta[FEW ? u : 0][e]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; e++) v[u][e] *= rstd;
+                for (int e = 0; e < 8; e++) v[u][e] *= normed.rest;
             }
             top[u] = fg_row16_max(absmax8(v[u]));
         }
@@ -300,12 +324,10 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
     Raw8 raw[4], w;
 #pragma unroll
     for (int i = 0; i < 4; i++) raw[i].load(at_elem(p.x, (r0 + i) * p.ld, p.x_bf16), (uint32_t)col, p.x_bf16);
-    float mean[4], rstd[4], gamma[8], beta[8], y[4][8];
+    float gamma[8], beta[8], y[4][8];
+    Normed<LAYER> normed[4];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        rstd[i] = p.rstd[r0 + i];
-        mean[i] = LAYER ? p.mean[r0 + i] : 0.0f;
-    }
+    for (int i = 0; i < 4; i++) normed[i].set(LAYER ? p.mean[r0 + i] : 0.0f, p.rstd[r0 + i]);
     w.load(p.gamma, col, p.w_bf16);
     w.get(gamma, p.w_bf16);
     if (p.beta) {
@@ -317,8 +339,8 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
         raw[i].get(y[i], p.x_bf16);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const float t = (LAYER ? y[i][e] - mean[i] : y[i][e]) * gamma[e];
-            y[i][e] = p.beta ? __builtin_fmaf(t, rstd[i], beta[e]) : t * rstd[i];
+            const float t = normed[i].gained(y[i][e], gamma[e]);
+            y[i][e] = p.beta ? __builtin_fmaf(t, normed[i].rest, beta[e]) : t * normed[i].rest;
         }
     }
     float top[4], s[4], m[8];

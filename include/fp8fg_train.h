@@ -30,8 +30,9 @@ typedef enum { FG_NORM_LAYER = 0, FG_NORM_RMS = 1 } fg_norm_kind;
  *   y       NULL, or bf16 [rows][cols], rounded from fp32.
  *   mean, rstd  f32 [rows] each, for the backward pass. mean may be NULL; it is written by FG_NORM_LAYER only. rstd may be
  *           NULL. With q_rows rstd has to be there, and with FG_NORM_LAYER mean too.
- *   Statistics, y and maxima are fp32. A row that holds a NaN or an infinity, or whose sums overflow fp32, gets NaN codes,
- *   under finite scales; with q_rows its values are NaN codes there too, and the other rows are as without it.
+ *   Statistics, y and maxima are fp32. A row that holds a NaN or an infinity, or whose sums (of LAYER's squares about the mean, of RMS's
+ *   squares) overflow fp32, gets NaN codes, under finite scales; with q_rows its values are NaN codes there too, and the other rows are
+ *   as without it. gamma and beta may be as large or small as fp32 allows, as long as y is finite.
  *   cols % 128 == 0, cols <= 18432; rows % 128 == 0 where q_rows is asked for, any rows otherwise; rows <= 2^25, and
  *   rows * cols < 2^36 where q_rows is asked for. eps finite and > 0. x, gamma, beta, q_cols, q_rows, y 16-byte aligned,
  *   ld_x a multiple of 16 bytes; the fp32 outputs 4-byte aligned. rows == 0 or cols == 0 is a no-op. Outputs must not
@@ -44,6 +45,7 @@ fg_status fg_norm_quantize(const void* x, fg_out_dtype x_type, int64_t ld_x, int
 /* Backward of the norm. With xhat = (x - mean) rstd (RMS: x rstd) and t = dy gamma,
  *   dx = rstd (t - mean(t) - xhat mean(t xhat)) + dres (RMS: without mean(t)),
  *   dgamma = column sums of dy xhat, dbeta = column sums of dy.
+ * All in fp32: t, t xhat and their sums over a row have to stay in its range, or the row's dx is not finite.
  *   x, gamma  as for fg_norm_quantize; mean, rstd f32 [rows], as it wrote them (mean not read, and may be NULL, with
  *             FG_NORM_RMS).
  *   dy        [rows][cols] of type dy_type, row stride ld_dy: the Dgrad of the Linear behind the norm.
