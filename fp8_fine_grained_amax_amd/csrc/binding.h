@@ -3,9 +3,13 @@
 #pragma once
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/record_function.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -17,6 +21,7 @@
 #include "fp8fg.h"
 
 inline PyObject* g_error = nullptr;      // the package's exception type
+inline thread_local bool g_watched = false;      // watched() at the entry of this thread's call: once, as it takes 0.05 us
 
 // A Python exception is set; unwinds to the entry. One type for all files: the entries are in another file than some of the
 // functions that throw it.
@@ -113,8 +118,21 @@ int flag(PyObject* o) {
 }
 fg_scale_mode mode(PyObject* pow2) { return flag(pow2) ? FG_SCALE_POW2 : FG_SCALE_FP32; }
 
-// Past torch's dispatcher, which took 0.2 of 0.65 us a tensor.
+// Whether somebody is to see an allocation: a dispatch mode or another layer of this thread, a profiler, or torch's fill of new
+// memory in its deterministic mode.
+bool watched() {
+    return !(c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set).empty() || at::hasCallbacks() ||
+           at::globalContext().deterministicAlgorithms();
+}
+// Held over a call, whose allocations may themselves call Python, and that another call.
+struct Watch {
+    const bool before = g_watched;
+    Watch() { g_watched = watched(); }
+    ~Watch() { g_watched = before; }
+};
+// Past torch's dispatcher where nobody watches, as it took 0.2 of 0.65 us a tensor.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, c10::Device d) {
+    if (g_watched) return at::empty(shape, at::TensorOptions(type).device(d));
     return at::Tensor(at::detail::empty_cuda(shape, type, d, std::nullopt));
 }
 // The caller's output buffer, or a new one.

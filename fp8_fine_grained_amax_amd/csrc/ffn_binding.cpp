@@ -172,6 +172,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", ARGS, n);
         return nullptr;
     }
+    const Watch watch;
     try {
         return F(args);
     } catch (const Raised&) {
