@@ -14,13 +14,12 @@
 // X itself: 8 x 2048 x 7168 4.02 ms against 3.85, 7168 x 18432 12.67 and 12.44, 512 x 1024 by 8 155 us and 144.)
 // Contractions are padded with zeros to multiples of 64.
 #include "host_util.h"
+#include "mfma_tile.h"
 #include "ortho_shape.h"
 #include "train_launch.h"
 
 #include <algorithm>
 #include <type_traits>
-
-#include "common.h"
 
 namespace {
 
@@ -52,31 +51,10 @@ struct OrthoGemm {
     int tiles, m_tiles;                          // of a matrix, and rows of them; tiles of 256 with a count
 };
 
-__device__ __forceinline__ int swz128(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base) {
-    const uint64_t u = (uint64_t)base;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)u);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(u >> 32));
-    return __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), (short)0, (int)0xFFFFFFFFu, 0x00020000);
-}
-// Compiled in the device pass only: the host pass does not know the 16-byte form.
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rs, void* lds, uint32_t voffset) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, FG_LDS(lds), 16, voffset, 0, 0, 0);
-#endif
-}
-
 typedef short v4s __attribute__((ext_vector_type(4)));
 // The transposing read. (restrict: without it the compiler waits for all loads to LDS before each.)
 __device__ __forceinline__ v2i tr_read(const uint8_t* __restrict__ lds) {
     return __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)lds));
-}
-
-// Workgroup b runs on XCD b % 8: every XCD gets one contiguous range of tile ids.
-__device__ __forceinline__ int xcd_remap(int b, int total) {
-    const int x = b & 7, base = total >> 3, extra = total & 7;
-    return x * base + (x < extra ? x : extra) + (b >> 3);
 }
 
 // Tile number id (below 2^24) of a lower triangle, row by row: the root is off by one at most.
@@ -160,11 +138,6 @@ __device__ __forceinline__ void big_tile(const OrthoGemm& p, int id, int64_t& ba
         ti = first + within % rows;
         tj = within / rows;
     }
-}
-
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
 template <class T>
@@ -310,11 +283,11 @@ __device__ __forceinline__ void mid_tile(const OrthoGemm& p, v4f* parts, int spl
     auto issue = [&](int kb, int slot) {
         const int k = kb < nkb ? kb : nkb - 1;
         uint8_t* st = smem + slot * C::STAGE;
-        const auto ra = buffer_rsrc(pp + (int64_t)k * 128), rb = buffer_rsrc(qp + k * q_step<P>(p));
+        const auto ra = fg_buffer_rsrc(pp + (int64_t)k * 128), rb = fg_buffer_rsrc(qp + k * q_step<P>(p));
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            load_lds16(ra, st + (wave + 4 * u) * 1024, a_off[u]);
-            load_lds16(rb, st + C::BM * 128 + (wave + 4 * u) * 1024, b_off[u]);
+            fg_buffer_load_lds16(ra, st + (wave + 4 * u) * 1024, a_off[u]);
+            fg_buffer_load_lds16(rb, st + C::BM * 128 + (wave + 4 * u) * 1024, b_off[u]);
         }
     };
     const int lrow = lane & 15, g16 = lane >> 4;
@@ -440,14 +413,14 @@ __device__ __forceinline__ void large_tile(const OrthoGemm& p, v4f* parts, int s
             b_off[h][u] = q_offset<P, C::BN>(p, n0, b_part(h, u), lane);
         }
     auto load_a = [&](int kb, int half) {
-        const auto rs = buffer_rsrc(pp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
+        const auto rs = fg_buffer_rsrc(pp + (int64_t)(kb < nkb ? kb : nkb - 1) * 128);
 #pragma unroll
-        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + a_row(half, u) * 128, a_off[half][u]);
+        for (int u = 0; u < 2; u++) fg_buffer_load_lds16(rs, smem + (kb & 1) * C::STAGE + a_row(half, u) * 128, a_off[half][u]);
     };
     auto load_b = [&](int kb, int half) {
-        const auto rs = buffer_rsrc(qp + (kb < nkb ? kb : nkb - 1) * q_step<P>(p));
+        const auto rs = fg_buffer_rsrc(qp + (kb < nkb ? kb : nkb - 1) * q_step<P>(p));
 #pragma unroll
-        for (int u = 0; u < 2; u++) load_lds16(rs, smem + (kb & 1) * C::STAGE + C::BM * 128 + b_part(half, u) * 1024, b_off[half][u]);
+        for (int u = 0; u < 2; u++) fg_buffer_load_lds16(rs, smem + (kb & 1) * C::STAGE + C::BM * 128 + b_part(half, u) * 1024, b_off[half][u]);
     };
 
     const int lrow = lane & 15, g16 = lane >> 4;
@@ -576,11 +549,11 @@ __device__ __forceinline__ void small_tile(const OrthoGemm& p, v4f* parts, int s
     }
     auto issue = [&](int kb, int slot) {
         if (kb >= nkb) return;
-        const auto ra = buffer_rsrc(pp + (int64_t)kb * 128), rb = buffer_rsrc(qp + kb * q_step<P>(p));
+        const auto ra = fg_buffer_rsrc(pp + (int64_t)kb * 128), rb = fg_buffer_rsrc(qp + kb * q_step<P>(p));
 #pragma unroll
         for (int u = 0; u < 8; u++) {
-            load_lds16(ra, ring + slot * C::STAGE + u * 1024, a_off[u]);
-            load_lds16(rb, ring + slot * C::STAGE + C::SIDE * 128 + u * 1024, b_off[u]);
+            fg_buffer_load_lds16(ra, ring + slot * C::STAGE + u * 1024, a_off[u]);
+            fg_buffer_load_lds16(rb, ring + slot * C::STAGE + C::SIDE * 128 + u * 1024, b_off[u]);
         }
     };
     const int lrow = lane & 15, g16 = lane >> 4;
