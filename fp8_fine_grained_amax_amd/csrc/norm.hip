@@ -143,8 +143,9 @@ struct Place {
 // contiguous) meet in lines of its own L2; without, rows are dealt in turn, so that the last ones are those that the Infinity
 // Cache still holds when the second kernel begins with them.
 //
-// 4096 x 7168 bf16, columns' tiles: 22 us, 4.1 TB/s (a copy of x takes 21 us); without its loads or its stores 18 to 20, so
-// HBM, sums and quantization overlap and none of them alone bounds it. 4096 x 18432 f32: 85 us, 4.5 TB/s; there HBM does.
+// 4096 x 7168 bf16, columns' tiles: RMS 22.5 us, 4.0 TB/s (a copy of x takes 21 us; with x from HBM 24.5), layer 28, with beta 27.4 to 32;
+// without its loads or its stores RMS takes 18 to 20, so HBM, sums and quantization overlap and none of them alone bounds it.
+// 4096 x 18432 f32: 85 us, 4.5 TB/s; there HBM does.
 //
 // FEW rows: a thread has as few groups as 16 waves a row allow, and gamma and beta in registers; a call's time is the latency
 // of its loads (one row of 1024: 2.3 us). Many: two groups (three past 16384 columns), so that what a row costs besides its elements
@@ -307,8 +308,8 @@ __global__ __launch_bounds__(64 * (FEW ? max_waves(U) : 16)) void fg_norm_kernel
 // Forward, both tilings and the output: a 512-thread workgroup takes 128 rows x 128 columns and reads x again (from the Infinity
 // Cache where it fits, hence the last rows first), with the statistics of the kernel above. Thread t holds rows 4 (t / 16) + i
 // of the eight columns t % 16: a row's tile is a DPP row, while the columns' maxima and codes go through LDS. HBM bounds it: 4096
-// x 7168 bf16 22.7 us, x from the cache, 117 MB in all; 4096 x 18432 f32 76.8 us, 453 MB, 5.9 TB/s. The statistics before it: 10.5
-// and 73.9 us (5.6 and 4.1 TB/s).
+// x 7168 bf16 23.2 us, x from the cache, 117 MB in all; 4096 x 18432 f32 75.7 us, 453 MB, 6.0 TB/s. The statistics before it: 10.6
+// and 73.0 us (5.5 and 4.1 TB/s).
 // ------------------------------------------------------------------------------------------------
 template <bool LAYER>
 __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
@@ -406,9 +407,10 @@ __global__ __launch_bounds__(512) void fg_norm_tiles_kernel(FgNorm p) {
 // no atomics, so that the result depends on the sizes only.
 //
 // HBM bounds it: x, dy and the residual's gradient are read once and dx is written (inputs bf16, f32, bf16; dx bf16). Up to
-// 8192 columns the next row is loaded while this one is worked on: 4096 x 7168 58 us, 5.0 TB/s; 16384 x 2048 58 us, 5.7 TB/s
-// (a copy reaches 4.7 to 5.2). With two and three groups a thread the registers do not hold a second row: 4096 x 12288 108 us,
-// 4.7 TB/s, 4096 x 18432 160 us, 4.7 TB/s. The second launch takes 2.5 to 5 us. Few rows are bound by latency, so they take one
+// 8192 columns the next row is loaded while this one is worked on: 4096 x 7168 62 us, 4.7 TB/s; 16384 x 2048 68 us, 4.9 TB/s
+// (a copy reaches 4.7 to 5.2). With two and three groups a thread the registers do not hold a second row: 4096 x 12288 122 us,
+// 4.1 TB/s, 4096 x 18432 179 us, 4.2 TB/s. (With the same inputs again and again, part of which the Infinity Cache then holds,
+// 58, 58, 108 and 160 us.) The second launch takes 2.5 to 5 us. Few rows are bound by latency, so they take one
 // launch, in which other workgroups read x and dy once more for the columns' sums.
 // ------------------------------------------------------------------------------------------------
 // Columns of a workgroup that sums them by itself. 64 and 128: 256 x 1024 f32 5.3 and 6.4 us, 512 x 1024 7.0 and 9.9, 64 x 18432
@@ -545,7 +547,7 @@ __global__ __launch_bounds__(64 * max_waves(U)) void fg_norm_bwd_kernel(FgNormBw
             load(row, rx, rd);
         }
         const float rstd = next_rstd, mean = next_mean;
-        if constexpr (AHEAD) load(row + at.groups, nx, nd);     // behind the last row it again: a branch costs 58 -> 65 us at 4096 x 7168
+        if constexpr (AHEAD) load(row + at.groups, nx, nd);     // behind the last row it again: a branch costs 12% at 4096 x 7168
         float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
         for (int u = 0; u < U; u++) {
@@ -761,7 +763,7 @@ hipError_t fg_launch_norm(const FgNorm& p, hipStream_t stream) {
         // x 12288 41.8 and 36.7, 4096 x 7168 both 22, but 16384 x 2048 21.5 and 23.0 and three groups (4096 x 18432) 49.1 and 51.4; f32 6000
         // x 5632 36.1 and 38.7; the statistics alone 4096 x 18432 f32 145 and 146.
         const int resident = TILES && p.x_bf16 && u == 2 && p.cols > 2048 ? 24 : 16;
-        // no more workgroups than a CU's 160 KB hold the weights of: with beta, 4096 x 7168 26.5 us, with three of them, of which two fit, 31
+        // no more workgroups than a CU's 160 KB hold the weights of: with beta, 4096 x 7168 27 us, with three of them, of which two fit, 31
         const int64_t held = TILES ? (160 * 1024) / (p.cols * (p.beta ? 8 : 4) + 512) : 16;
         const int64_t fill = cus * std::max<int64_t>(1, std::min<int64_t>(resident / (waves * groups), held));
         switch (u) {

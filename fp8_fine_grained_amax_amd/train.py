@@ -74,6 +74,7 @@ def fg_norm_bwd(x, mean, rstd, gamma, dy, residual_grad=None, kind: int = FG_NOR
 def fg_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, scale: float = 1.0, out=None,
                      workspace=None):
     """Orthogonalised update by Newton-Schulz products: of each matrix of g (f32 or bf16, [N, K] or [batch, N, K]), X = g / (|g| +
-    eps), `steps` times X = (a I + b A + c A A) X with A = X X^T, and scale X as bf16."""
+    eps), `steps` times X = (a I + b A + c A A) X with A = X X^T, and scale X as bf16. X, A and the sum in brackets are held in fp16;
+    fp8fg_train.h says how exact that leaves updates of gradients with different spectra."""
     a, b, c = coefficients
     return _ffn().orthogonalize(g, steps, a, b, c, eps, scale, out, workspace)
